@@ -59,9 +59,17 @@ class DeviceGuard {
 
   // A stream created on another device than the bound one cannot run this
   // call's kernels: MOE_ERR_INVALID_ARG.  The legacy and per-thread default
-  // streams (and NULL) belong to whichever device is current.
+  // streams (and NULL) belong to whichever device is current.  A stream that
+  // is being captured cannot be asked for its device (the question itself
+  // invalidates the capture): there a wrong device shows as a failed launch.
   moe_status check_stream(cudaStream_t s) const {
     if (s == nullptr || s == cudaStreamLegacy || s == cudaStreamPerThread) return MOE_OK;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) {
+      cudaGetLastError();
+      return MOE_ERR_INVALID_ARG;
+    }
+    if (cap != cudaStreamCaptureStatusNone) return MOE_OK;
     int sd = -1;
     if (cudaStreamGetDevice(s, &sd) != cudaSuccess) {
       cudaGetLastError();
