@@ -65,11 +65,16 @@
  *    word and returns; it never traps.
  *  - Calls that share a workspace must not overlap on the GPU.
  *  - Device: a call runs on the device that owns its workspace (moe_combine:
- *    y; moe_quantize_e4m3: blob; moe_permute_noalloc: counts), making it
+ *    y; moe_quantize_e4m3: blob; moe_permute_noalloc: counts; the entry points
+ *    below that take no workspace name theirs), making it
  *    current for the duration of the call and restoring the caller's current
  *    device before returning.  x (moe_forward) must live on that device, and
  *    a stream created on another device is rejected (MOE_ERR_INVALID_ARG);
  *    NULL and the legacy / per-thread default streams are the bound device's.
+ *  - Every entry point but moe_device_status may be captured into a CUDA graph
+ *    (of a stream under capture the device is not checked); a graph's replays
+ *    use the buffers of the captured call, so they must not overlap other
+ *    calls that share its workspace.
  *  - Failure injection (tests): with the environment variable MOE_FAULT set to
  *    "launch", every entry point that would launch work returns MOE_ERR_CUDA
  *    after its host-side checks and before any CUDA call, so nothing runs.
@@ -332,6 +337,79 @@ moe_status moe_forward_traced(const moe_config* cfg, const void* x, const void* 
                               int32_t* opt_topk_ids, float* opt_topk_w, int32_t* opt_counts,
                               void* ws, size_t ws_bytes, moe_stream_t stream,
                               const moe_event_t* stage_events);
+
+/* ---------------------------------------------------------------- routing from logits
+   For callers that have the router's logits (a router run elsewhere, in
+   another precision, or one that is being trained): group-limited selection
+   with a balance bias on the scores, and the gradients.  Per token, over the
+   experts that are available (below):
+     score    s_i = sigmoid(l_i), or the softmax of l over the available experts
+     choice   c_i = s_i + b_i        (b: optional per-expert bias, selection only;
+              "Mixture of experts: how MoE works and what it costs", "Why load
+              balancing is the hard part of MoE")
+     groups   the experts form n_groups equal blocks of neighbours; a group's
+              score is its largest choice, or the sum of its two largest; only
+              the topk_groups best groups stay (ties -> the lower group)
+     top-k    the k largest choices in them, descending, ties -> lower index
+     weights  scale * s_i, divided by the sum over the picked when renormalised
+   Available: a logit above the lowest finite value of its type; -inf, NaN and
+   that value (the usual masks) exclude an expert for that token, and so does a
+   bias of -inf or NaN.  +inf counts as the largest finite value.  A slot for
+   which no expert is left gets id -1 and weight 0, so a row masked throughout
+   (padding) routes nowhere.  Choices are compared as the stored logits define
+   them: without a bias (or with zeros) by their logits, otherwise in binary64
+   wherever fp32 could not tell. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  int64_t T;                /* tokens                                          */
+  int64_t logits_stride;    /* elements between rows of the logits and of
+                               their gradient; 0 = n_experts                   */
+  int32_t n_experts;        /* E, 1..1024                                      */
+  int32_t top_k;            /* k, 1..min(16, topk_groups * E / n_groups)       */
+  int32_t n_groups;         /* divides E, 1..32; 1: no groups                  */
+  int32_t topk_groups;      /* groups kept, 1..n_groups                        */
+  int32_t group_top;        /* group score: 1 its largest choice, 2 the sum of
+                               its two largest (the one that is left, if one)  */
+  int32_t score;            /* moe_score                                       */
+  int32_t renormalise;      /* 0 or 1                                          */
+  int32_t logits_dtype;     /* moe_dtype of the logits and of their gradient   */
+  float weight_scale;       /* finite                                          */
+  int32_t reserved;         /* 0                                               */
+} moe_route_config;
+
+/* logits [T, E] (rows logits_stride apart), select_bias [E] fp32 or NULL
+   -> topk_ids [T, k] int32, topk_w [T, k] fp32.  Needs no workspace.  The call
+   runs on the device that owns topk_ids; logits must live there. */
+moe_status moe_route_topk(const moe_route_config* cfg, const void* logits, const float* select_bias,
+                          int32_t* topk_ids, float* topk_w, moe_stream_t stream);
+
+/* The gradient with respect to the logits of
+     sum grad_w * topk_w  +  balance_coef * L_balance  +  z_coef * L_z
+   with topk_w the weights moe_route_topk gives for topk_ids, and L_balance and
+   L_z the penalties of moe_router_aux_losses on these logits (means over all T
+   rows; the softmax runs over the available experts, and a row without any
+   adds nothing; the shares counts[e] / sum(counts) are constants).
+   topk_ids [T, k] and grad_w [T, k] fp32: both given, or grad_w NULL (no
+   weights' term).  Ids outside [0, E) are empty slots.  counts [E] int32: needed
+   when balance_coef is not 0.  grad_logits: rows and type of the logits; every
+   column of the E is written (0 where an expert is not available), what lies
+   between the rows is not touched; it must not overlap the logits.  Deterministic.  Runs on the device of grad_logits. */
+moe_status moe_route_backward(const moe_route_config* cfg, const void* logits, const int32_t* topk_ids,
+                              const float* grad_w, const int32_t* counts, float balance_coef, float z_coef,
+                              void* grad_logits, moe_stream_t stream);
+
+/* The gradients of moe_combine: from grad_y [T, d], the experts' rows y_perm
+   [T*k, d], row_of and topk_w of the forward call
+     grad_y_perm[row_of[t*k+s]] = topk_w[t,s] * grad_y[t]     (dtype)
+     grad_w[t,s] = <grad_y[t], y_perm[row_of[t*k+s]]>         (fp32; 0 for a dropped slot)
+   Either output may be NULL (y_perm is only read for grad_w, topk_w only for
+   grad_y_perm; they may then be NULL too).  Rows that no slot points at are
+   left as they were.  The shared experts' gradient is grad_y itself.
+   Deterministic.  Runs on the device of grad_y. */
+moe_status moe_combine_backward(const moe_config* cfg, const void* grad_y, const void* y_perm,
+                                const int32_t* row_of, const float* topk_w, void* grad_y_perm, float* grad_w,
+                                moe_stream_t stream);
 
 /* Synchronises `stream` and returns the status word of `ws`: MOE_OK,
    MOE_ERR_TIMEOUT or MOE_ERR_BAD_EXPERT_ID (or MOE_ERR_CUDA). */

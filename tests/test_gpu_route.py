@@ -1,0 +1,390 @@
+"""Routing from logits, its gradient and the combine's gradient on the GPU,
+against the float64 oracle.
+
+Tolerances.  One fp32 operation is off by u = 2^-24 of its result, expf by at
+most 4 u.  A weight is a quotient of an exponential (its argument, a
+difference of order 10, off by 10 u) and a sum of such (at most 37 additions):
+below 2 (10 + 4 + 2) + 37 + 3 < 80 u.  Gradients multiply two or three such
+factors and subtract sums of k or E of them: below 200 u of the largest term.
+The last rounding is half a step: u in fp32, 2^-8 in bf16.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import top_routing_expert_gemm_b200 as moe
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF_STEP = {"f32": U, "bf16": 2.0 ** -8}
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+SCORE = {"sigmoid": moe.MOE_SCORE_SIGMOID, "softmax": moe.MOE_SCORE_SOFTMAX}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def _f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _logits(T, E, dtype, seed, masks=0.0, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    wide = torch.full((T, E + pad), 99.0).to(DT[dtype])
+    l = torch.randn(T, E, generator=g)
+    if masks:
+        off = torch.rand(T, E, generator=g) < masks
+        kind = torch.randint(0, 3, (T, E), generator=g)
+        l = l.to(DT[dtype])
+        low = torch.finfo(DT[dtype]).min
+        for i, v in enumerate((float("-inf"), float("nan"), low)):
+            l[off & (kind == i)] = v
+        if T > 2:
+            l[T - 1] = low  # a padding row
+            l[T // 2] = float("-inf")
+    wide[:, :E] = l.to(DT[dtype])
+    return wide.cuda()[:, :E]
+
+
+def _cfg(l, k, score, G=1, Gk=1, gtop=1, renorm=1, scale=1.0):
+    return moe.make_route_config(l.shape[0], l.shape[1], k, SCORE[score], G, Gk, gtop, renorm, scale,
+                                 moe.MOE_BF16 if l.dtype == torch.bfloat16 else moe.MOE_F32, l.stride(0))
+
+
+def _run(l, bias, cfg):
+    ids = torch.full((cfg.T, cfg.top_k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((cfg.T, cfg.top_k), float("nan"), device="cuda")
+    moe.moe_route_topk(cfg, l, bias, ids, w)
+    torch.cuda.synchronize()
+    return ids, w
+
+
+def _check(l, bias, cfg, score, ids, w, dtype):
+    want_ids, want_w, gap = oracle.route_logits(_f64(l), None if bias is None else _f64(bias), cfg.top_k, score,
+                                                cfg.n_groups, cfg.topk_groups, cfg.group_top, bool(cfg.renormalise),
+                                                float(cfg.weight_scale), dtype)
+    sure = (gap > 1e-13) | (gap == 0.0)  # binary64 sums of two scores: a few 2^-53
+    assert sure.mean() > 0.99
+    got = ids.cpu().numpy()
+    assert np.array_equal(got[sure], want_ids[sure])
+    gw = _f64(w)
+    assert np.all(np.abs(gw[sure] - want_w[sure]) <= 80 * U * want_w[sure] + 1e-37)
+    return want_ids
+
+
+SHAPES = [  # E, k, G, Gk, group_top
+    (1, 1, 1, 1, 1), (5, 2, 1, 1, 1), (8, 2, 1, 1, 1), (60, 6, 1, 1, 1), (128, 4, 1, 1, 1), (256, 8, 8, 4, 2),
+    (256, 8, 8, 4, 1), (160, 6, 8, 3, 2), (160, 6, 8, 3, 1), (64, 16, 32, 9, 2), (96, 5, 3, 2, 2), (256, 4, 2, 1, 2),
+    (384, 8, 1, 1, 1), (1000, 13, 10, 3, 2), (1024, 16, 16, 4, 2), (32, 4, 32, 5, 2), (30, 3, 15, 4, 1),
+]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k,G,Gk,gtop", SHAPES)
+@pytest.mark.parametrize("dtype,bias,masks,pad", [("f32", True, 0.0, 0), ("bf16", False, 0.3, 3),
+                                                  ("f32", False, 0.1, 8), ("bf16", True, 0.7, 0)])
+def test_route_matches_the_oracle(score, E, k, G, Gk, gtop, dtype, bias, masks, pad):
+    l = _logits(53, E, dtype, E + k, masks, pad)
+    b = (0.2 * torch.randn(E, generator=torch.Generator().manual_seed(1))).cuda() if bias else None
+    renorm, scale = (1, 2.5) if (E + pad) % 2 else (int(score == "sigmoid"), 1.0)
+    cfg = _cfg(l, k, score, G, Gk, gtop, renorm, scale)
+    ids, w = _run(l, b, cfg)
+    _check(l, b, cfg, score, ids, w, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 129, 20011])
+def test_route_batch_sizes(T):
+    """One row, odd batches, and more rows than the grid has warps."""
+    l = _logits(T, 64, "f32", T)
+    b = (0.1 * torch.randn(64, generator=torch.Generator().manual_seed(2))).cuda()
+    cfg = _cfg(l, 6, "sigmoid", 8, 3, 2, 1, 2.5)
+    ids, w = _run(l, b, cfg)
+    rows = torch.arange(T)[:: max(1, T // 500)]
+    sub = l[rows.cuda()]
+    _check(sub, b, _cfg(sub, 6, "sigmoid", 8, 3, 2, 1, 2.5), "sigmoid", ids[rows.cuda()], w[rows.cuda()], "f32")
+    again, w2 = _run(l, b, cfg)
+    assert torch.equal(ids, again) and torch.equal(w, w2)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("G,Gk,gtop", [(1, 1, 1), (8, 3, 2), (8, 3, 1)])
+def test_choices_closer_than_fp32_are_decided_as_the_logits_say(score, G, Gk, gtop):
+    """A bias that cancels the scores to within half an fp32 step: every order
+    hangs on bits that fp32 scores do not have."""
+    T, E, k = 96, 64, 8
+    rng = np.random.default_rng(9)
+    base = rng.standard_normal(E).astype(np.float32)
+    l = np.repeat(base[None], T, 0)
+    for _ in range(3):  # rows a few fp32 steps apart
+        l = np.where(rng.random((T, E)) < 0.3, np.nextafter(l, np.float32(9)), l)
+    s = oracle.route_scores(base.astype(np.float64), score)
+    bias = torch.from_numpy((0.5 - s).astype(np.float32)).cuda()
+    lt = torch.from_numpy(l).cuda()
+    cfg = _cfg(lt, k, score, G, Gk, gtop)
+    ids, w = _run(lt, bias, cfg)
+    _check(lt, bias, cfg, score, ids, w, "f32")
+
+
+def test_ties_zero_bias_and_equal_rows_take_the_lowest_index():
+    for E, G, Gk, gtop in ((40, 1, 1, 1), (64, 8, 2, 2), (30, 5, 2, 2)):
+        l = torch.zeros(9, E, device="cuda")
+        l[3:, 7] = 1.0
+        for bias in (None, torch.zeros(E, device="cuda"), torch.full((E,), 0.25, device="cuda")):
+            for score in ("sigmoid", "softmax"):
+                cfg = _cfg(l, 3, score, G, Gk, gtop)
+                ids, w = _run(l, bias, cfg)
+                assert ids[:3].eq(torch.arange(3, device="cuda", dtype=torch.int32)).all()
+                _check(l, bias, cfg, score, ids, w, "f32")
+
+
+def test_extreme_logits_and_biases():
+    inf, nan, low = float("inf"), float("nan"), torch.finfo(torch.float32).min
+    l = torch.tensor([[inf, 1.0, -2.0, inf, 0.0], [-900.0, -901.0, -2000.0, low, nan], [1e30, -1e30, 3.0, 2.0, 1e30],
+                      [-0.0, 0.0, -1e-40, 1e-40, -inf], [low, nan, -inf, low, nan], [88.0, 89.0, 300.0, -88.0, -300.0]],
+                     device="cuda")
+    for score in ("sigmoid", "softmax"):
+        for renorm in (0, 1):
+            cfg = _cfg(l, 3, score, renorm=renorm)
+            ids, w = _run(l, None, cfg)
+            # ranks by the logit: saturated scores do not tie
+            assert ids.cpu().tolist() == [[0, 3, 1], [0, 1, 2], [0, 4, 2], [3, 0, 1], [-1] * 3, [2, 1, 0]]
+            want_ids, want_w, _ = oracle.route_logits(_f64(l), None, 3, score, renormalise=bool(renorm))
+            assert np.all(np.abs(_f64(w) - want_w) <= 80 * U * want_w + 1e-37)
+    b = torch.tensor([-inf, nan, inf, inf, -3.0], device="cuda")
+    ids, w = _run(torch.zeros(2, 5, device="cuda"), b, _cfg(torch.zeros(2, 5, device="cuda"), 4, "softmax"))
+    assert ids.cpu().tolist() == [[2, 3, 4, -1]] * 2
+    assert torch.allclose(w, torch.tensor([[1 / 3, 1 / 3, 1 / 3, 0.0]], device="cuda").expand(2, 4))
+
+
+def test_rows_past_32_bit_offsets():
+    """Row strides that take the last rows past 2^32 bytes and 2^31 elements."""
+    T, E, stride = 2100, 16, 1 << 20
+    wide = torch.empty(T * stride, dtype=torch.bfloat16, device="cuda")
+    l = torch.as_strided(wide, (T, E), (stride, 1))
+    l.copy_(_logits(T, E, "bf16", 5))
+    cfg = _cfg(l, 2, "softmax")
+    assert (T - 1) * stride > 2 ** 31
+    ids, w = _run(l, None, cfg)
+    dense = l.contiguous()
+    ids2, w2 = _run(dense, None, _cfg(dense, 2, "softmax"))
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+    _check(dense[-64:], None, _cfg(dense[-64:], 2, "softmax"), "softmax", ids[-64:], w[-64:], "bf16")
+    del wide, l
+    torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ gradient
+def _grad_check(l, ids, g, cfg, score, counts, balance, z, dtype, grad):
+    want = oracle.route_backward(_f64(l), ids.cpu().numpy(), None if g is None else _f64(g), score,
+                                 bool(cfg.renormalise), float(cfg.weight_scale),
+                                 None if counts is None else counts.cpu().numpy(), balance, z, dtype)
+    u = oracle.usable_logits(_f64(l), dtype)
+    top = np.max(np.where(u > -np.inf, u, -1e30), axis=1)
+    lse = np.where(top > -1e29, np.abs(top) + np.log(l.shape[1]), 0.0)
+    mag = abs(cfg.weight_scale) * (np.max(np.abs(_f64(g)), axis=1) if g is not None else 0.0) \
+        + abs(balance) * l.shape[1] / l.shape[0] + 2 * abs(z) / l.shape[0] * lse
+    tol = HALF_STEP[dtype] * np.abs(want) + 200 * U * np.broadcast_to(mag, (l.shape[0],))[:, None] + 1e-40
+    err = np.abs(_f64(grad) - want)
+    assert np.all(err <= tol), float(np.max(err / tol))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("E,k,G,Gk,gtop", [s for s in SHAPES if s[0] in (1, 5, 60, 128, 256, 1000)])
+@pytest.mark.parametrize("dtype,masks,pad,balance,z,weights", [
+    ("f32", 0.0, 0, 0.0, 0.0, True), ("bf16", 0.3, 3, 0.01, 0.001, True), ("f32", 0.2, 4, 0.5, 0.0, True),
+    ("bf16", 0.0, 8, 0.0, 0.25, True), ("f32", 0.5, 1, 0.5, 0.25, False)])
+def test_route_backward_matches_the_oracle(score, renorm, E, k, G, Gk, gtop, dtype, masks, pad, balance, z, weights):
+    l = _logits(41, E, dtype, E + 3 * k, masks, pad)
+    cfg = _cfg(l, k, score, G, Gk, gtop, renorm, 2.5)
+    ids, _ = _run(l, None, cfg)
+    g = torch.randn(41, k, generator=torch.Generator().manual_seed(3)).cuda()
+    if weights:
+        g[ids < 0] = float("nan")  # an empty slot's gradient is never used
+    counts = torch.bincount(ids[ids >= 0].long(), minlength=E).int()
+    out = torch.full((41, E + pad), 77.0, dtype=l.dtype, device="cuda")
+    grad = out[:, :E]
+    moe.moe_route_backward(cfg, l, ids, g if weights else None, counts if balance else None, balance, z, grad)
+    torch.cuda.synchronize()
+    assert out[:, E:].eq(77.0).all()
+    if weights:
+        g = torch.nan_to_num(g)
+    _grad_check(l, ids, g if weights else None, cfg, score, counts, balance, z, dtype, grad)
+
+
+def test_route_backward_repeated_and_stray_ids():
+    """Ids of the caller's own: a repeated id adds up, one outside [0, E) is an
+    empty slot, one on a masked expert has no gradient."""
+    l = torch.randn(6, 10, generator=torch.Generator().manual_seed(4))
+    l[2, 5] = float("-inf")
+    l = l.cuda()
+    ids = torch.tensor([[1, 1, 3], [0, 9, 10], [5, 2, 1], [-1, -1, -1], [7, -3, 7], [2 ** 30, 4, 6]],
+                       dtype=torch.int32, device="cuda")
+    g = torch.randn(6, 3, generator=torch.Generator().manual_seed(5)).cuda()
+    for score in ("sigmoid", "softmax"):
+        for renorm in (0, 1):
+            cfg = _cfg(l, 3, score, renorm=renorm)
+            grad = torch.empty_like(l)
+            moe.moe_route_backward(cfg, l, ids, g, None, 0.0, 0.0, grad)
+            if renorm or score == "sigmoid":
+                _grad_check(l, ids, g, cfg, score, None, 0.0, 0.0, "f32", grad)
+            assert grad[3].eq(0).all() and grad[2, 5] == 0
+
+
+def test_route_backward_counts_of_zero_and_empty_terms():
+    l = torch.randn(4, 6, device="cuda")
+    ids = torch.full((4, 2), -1, dtype=torch.int32, device="cuda")
+    grad = torch.full_like(l, 9.0)
+    moe.moe_route_backward(_cfg(l, 2, "softmax"), l, ids, None, torch.zeros(6, dtype=torch.int32, device="cuda"), 1.0,
+                           0.0, grad)
+    assert grad.eq(0).all()
+    grad.fill_(9.0)
+    moe.moe_route_backward(_cfg(l, 2, "softmax"), l, None, None, None, 0.0, 0.0, grad)
+    assert grad.eq(0).all()
+
+
+# ------------------------------------------------------------------ combine
+def _dispatch(T, E, k, seed, cap=None):
+    rng = np.random.default_rng(seed)
+    ids = np.argsort(rng.random((T, E)), axis=1)[:, :k]
+    counts, offsets, perm, row_of = oracle.dispatch(ids, E, cap)
+    return ids, counts, offsets, perm, torch.from_numpy(np.asarray(row_of).reshape(-1).astype(np.int32)).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d,E,k,cap", [(1, 8, 4, 1, None), (37, 256, 8, 2, 5), (64, 520, 8, 3, None),
+                                         (33, 1000, 16, 16, 20), (19, 4096, 8, 8, None), (300, 2880, 32, 4, 30)])
+def test_combine_backward_matches_the_oracle(dtype, T, d, E, k, cap):
+    _, _, _, _, row_of = _dispatch(T, E, k, T + d, cap)
+    gen = torch.Generator().manual_seed(T)
+    gy = torch.randn(T, d, generator=gen).to(DT[dtype]).cuda()
+    yp = torch.randn(T * k, d, generator=gen).to(DT[dtype]).cuda()
+    w = torch.rand(T, k, generator=gen).cuda()
+    cfg = moe.make_config(T, d, E, k, 8, moe.MOE_BF16 if dtype == "bf16" else moe.MOE_F32, moe.MOE_SOFTMAX_TOPK)
+    rows = torch.full((T * k, d), 5.5, dtype=DT[dtype], device="cuda")
+    gw = torch.full((T, k), float("nan"), device="cuda")
+    moe.moe_combine_backward(cfg, gy, yp, row_of, w, rows, gw)
+    torch.cuda.synchronize()
+    want_rows, want_w = oracle.combine_backward(_f64(gy), _f64(yp), row_of.cpu().numpy(), _f64(w), k)
+    used = ~np.isnan(want_rows[:, 0])
+    got = _f64(rows)
+    assert np.all(got[~used] == 5.5)
+    assert np.all(np.abs(got[used] - want_rows[used]) <= (HALF_STEP[dtype] + 2 * U) * np.abs(want_rows[used]) + 1e-40)
+    absdot = np.array([[np.abs(_f64(gy[t])) @ np.abs(_f64(yp[max(0, int(row_of[t * k + s]))])) for s in range(k)]
+                       for t in range(T)])
+    assert np.all(np.abs(_f64(gw) - want_w) <= (d / 32 + 16) * U * absdot)
+    # either output alone gives the same
+    rows2, gw2 = torch.full_like(rows, 5.5), torch.empty_like(gw)
+    moe.moe_combine_backward(cfg, gy, None, row_of, w, rows2, None)
+    moe.moe_combine_backward(cfg, gy, yp, row_of, None, None, gw2)
+    assert torch.equal(rows, rows2) and torch.equal(gw, gw2)
+
+
+# ------------------------------------------------------------------ together
+def test_router_gradient_through_the_layer():
+    """route -> dispatch -> experts -> combine and back to the logits: the
+    chained gradient equals the oracle's on the rows the GPU computed, and the
+    layer's own outputs at logits +- h v differ as the oracle's do.
+
+    L = <grad_y, y>.  y is a k-term fp32 sum per element and w is off by 80 u:
+    a difference of two L is off by at most 2 * 90 u sum |grad_y||w y_perm|,
+    divided by 2 h."""
+    T, E, k, d, f = 48, 16, 4, 64, 96
+    gen = torch.Generator().manual_seed(11)
+    x = torch.randn(T, d, generator=gen).cuda()
+    l = torch.randn(T, E, generator=gen).cuda()
+    w_gu = (torch.randn(E, 2 * f, d, generator=gen) / d ** 0.5).cuda()
+    w_d = (torch.randn(E, d, f, generator=gen) / f ** 0.5).cuda()
+    gy = torch.randn(T, d, generator=gen).cuda()
+    bias = (0.1 * torch.randn(E, generator=gen)).cuda()
+    v = torch.randn(T, E, generator=gen).cuda()
+    route = _cfg(l, k, "sigmoid", 4, 2, 2, 1, 2.0)
+    cfg = moe.make_config(T, d, E, k, f, moe.MOE_F32, moe.MOE_SOFTMAX_TOPK)
+    ws = torch.zeros(moe.moe_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    ids, w = _run(l, bias, route)
+    counts = torch.empty(E, dtype=torch.int32, device="cuda")
+    offsets = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    perm = torch.empty(T * k, dtype=torch.int32, device="cuda")
+    row_of = torch.empty(T * k, dtype=torch.int32, device="cuda")
+    xp, yp = torch.empty(T * k, d, device="cuda"), torch.empty(T * k, d, device="cuda")
+    y = torch.empty(T, d, device="cuda")
+    moe.moe_permute(cfg, ids, x, counts, offsets, perm, row_of, xp, ws)
+    moe.moe_grouped_ffn(cfg, xp, offsets, w_gu, w_d, yp, ws)
+    gw, grad = torch.empty(T, k, device="cuda"), torch.empty(T, E, device="cuda")
+    moe.moe_combine_backward(cfg, gy, yp, row_of, w, None, gw)
+    moe.moe_route_backward(route, l, ids, gw, counts, 0.01, 0.001, grad)
+    assert moe.moe_device_status(ws) == 0
+    _, want_gw = oracle.combine_backward(_f64(gy), _f64(yp), row_of.cpu().numpy(), _f64(w), k)
+    want = oracle.route_backward(_f64(l), ids.cpu().numpy(), want_gw, "sigmoid", True, 2.0, counts.cpu().numpy(),
+                                 0.01, 0.001)
+    absw = np.array([[np.abs(_f64(gy[t])) @ np.abs(_f64(yp[int(row_of[t * k + s])])) for s in range(k)]
+                     for t in range(T)])
+    assert np.max(np.abs(_f64(grad) - want)) <= 200 * U * (2.0 * absw.max() + 1.0)
+
+    h = 2.0 ** -7
+
+    def layer(l2):  # same picks, weights of the shifted logits (k = E of the picked ones only)
+        w2 = torch.empty_like(w)
+        sub = torch.gather(l2, 1, ids.long()).contiguous()
+        ids2 = torch.empty_like(ids)
+        moe.moe_route_topk(_cfg(sub, k, "sigmoid", 1, 1, 1, 1, 2.0), sub, None, ids2, w2)
+        back = torch.empty_like(w2).scatter_(1, ids2.long(), w2)
+        moe.moe_combine(cfg, yp, row_of, back, None, y)
+        return float((gy.double() * y.double()).sum())
+
+    got = (layer(l + h * v) - layer(l - h * v)) / (2 * h)
+
+    def obj(l2):
+        return oracle.route_objective(l2, ids.cpu().numpy(), want_gw, "sigmoid", True, 2.0)
+    lp, lm = _f64(l + h * v), _f64(l - h * v)
+    want_diff = (obj(lp) - obj(lm)) / (2 * h)
+    bound = 2 * 90 * U * float(np.sum(absw * _f64(w))) / (2 * h)
+    assert abs(got - want_diff) <= bound
+    # and that difference is the gradient's, up to h^2 times a third derivative of order 1 per logit
+    flat = float(np.sum(oracle.route_backward(_f64(l), ids.cpu().numpy(), want_gw, "sigmoid", True, 2.0) * _f64(v)))
+    assert abs(want_diff - flat) <= h * h * float(np.sum(absw[:, :, None] * np.abs(_f64(v))[:, None, :] ** 3))
+
+
+def test_route_on_another_stream_and_in_a_graph():
+    T, E, k = 77, 256, 8
+    l = _logits(T, E, "f32", 1)
+    b = (0.1 * torch.randn(E, generator=torch.Generator().manual_seed(2))).cuda()
+    cfg = _cfg(l, k, "sigmoid", 8, 4, 2, 1, 2.5)
+    want_ids, want_w = _run(l, b, cfg)
+    g = torch.randn(T, k, device="cuda")
+    want_grad = torch.empty_like(l)
+    counts = torch.ones(E, dtype=torch.int32, device="cuda")
+    moe.moe_route_backward(cfg, l, want_ids, g, counts, 0.01, 0.001, want_grad)
+    ids, w, grad = torch.empty_like(want_ids), torch.empty_like(want_w), torch.empty_like(l)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    live = l.clone()
+    with torch.cuda.graph(graph, stream=side):
+        moe.moe_route_topk(cfg, live, b, ids, w)
+        moe.moe_route_backward(cfg, live, ids, g, counts, 0.01, 0.001, grad)
+    for shift in (0, 1):
+        live.copy_(l.roll(shift, 0))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ids, want_ids.roll(shift, 0)) and torch.equal(w, want_w.roll(shift, 0))
+    live.copy_(l)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(grad, want_grad)
+
+
+def test_route_refuses_host_tensors_and_keeps_outputs():
+    l = torch.randn(4, 8)
+    ids = torch.full((4, 2), -7, dtype=torch.int32, device="cuda")
+    w = torch.zeros(4, 2, device="cuda")
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_route_topk(_cfg(l, 2, "softmax"), l, None, ids, w)
+    assert e.value.status == 1
+    torch.cuda.synchronize()
+    assert ids.eq(-7).all()

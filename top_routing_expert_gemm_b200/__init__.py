@@ -17,6 +17,8 @@ __all__ = [
     "moe_quantize_e4m3", "moe_forward_traced", "MOE_W_NATIVE", "MOE_W_E4M3",
     "MOE_F32", "MOE_BF16", "MOE_SOFTMAX_ALL_RENORM", "MOE_SOFTMAX_TOPK", "MOE_SIGMOID_TOPK_RENORM",
     "MOE_SOFTMAX_ALL_NO_RENORM", "MOE_ACT_SWIGLU", "MOE_ACT_GELU",
+    "MoeRouteConfig", "make_route_config", "moe_route_topk", "moe_route_backward", "moe_combine_backward",
+    "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID",
     "EXPORTED_SYMBOLS", "LIB_PATH",
 ]
 
@@ -29,11 +31,13 @@ MOE_F32, MOE_BF16 = 0, 1
 MOE_SOFTMAX_ALL_RENORM, MOE_SOFTMAX_TOPK, MOE_SIGMOID_TOPK_RENORM, MOE_SOFTMAX_ALL_NO_RENORM = 0, 1, 2, 3
 MOE_ACT_SWIGLU, MOE_ACT_GELU = 0, 1
 MOE_W_NATIVE, MOE_W_E4M3 = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 EXPORTED_SYMBOLS = (
     "moe_workspace_bytes", "moe_status_string", "moe_router_topk", "moe_permute", "moe_grouped_ffn",
     "moe_combine", "moe_forward", "moe_device_status", "moe_permute_noalloc", "moe_expert_capacity",
     "moe_router_aux_losses", "moe_e4m3_weight_bytes", "moe_quantize_e4m3", "moe_forward_traced",
+    "moe_route_topk", "moe_route_backward", "moe_combine_backward",
 )
 
 
@@ -59,6 +63,23 @@ class MoeConfig(ctypes.Structure):
         ("wait_limit_ns", ctypes.c_int64),
         ("capacity_factor", ctypes.c_float),
         ("weight_format", ctypes.c_int32),
+    ]
+
+
+class MoeRouteConfig(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64),
+        ("logits_stride", ctypes.c_int64),
+        ("n_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("n_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("renormalise", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32),
+        ("weight_scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -91,6 +112,10 @@ def lib() -> ctypes.CDLL:
         L.moe_router_aux_losses.argtypes = [cfgp, vp, vp, vp, vp, vp, sz, vp]
         L.moe_e4m3_weight_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64]
         L.moe_quantize_e4m3.argtypes = [vp, ctypes.c_int64, ctypes.c_int32, vp, vp]
+        rcp, f32 = ctypes.POINTER(MoeRouteConfig), ctypes.c_float
+        L.moe_route_topk.argtypes = [rcp, vp, vp, vp, vp, vp]
+        L.moe_route_backward.argtypes = [rcp, vp, vp, vp, vp, f32, f32, vp, vp]
+        L.moe_combine_backward.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp]
         for name in EXPORTED_SYMBOLS[2:]:
             getattr(L, name).restype = i32
         L.moe_expert_capacity.restype = ctypes.c_int64
@@ -105,6 +130,13 @@ def make_config(T: int, d_model: int, n_experts: int, top_k: int, d_ff: int, dty
                 capacity_factor: float = 0.0, weight_format: int = MOE_W_NATIVE) -> MoeConfig:
     return MoeConfig(T, d_model, n_experts, top_k, d_ff, n_shared, d_ff_shared, dtype, gating,
                      bias_select_only, expert_act, wait_limit_ns, capacity_factor, weight_format)
+
+
+def make_route_config(T: int, n_experts: int, top_k: int, score: int, n_groups: int = 1, topk_groups: int = 1,
+                      group_top: int = 1, renormalise: int = 1, weight_scale: float = 1.0,
+                      logits_dtype: int = MOE_F32, logits_stride: int = 0) -> MoeRouteConfig:
+    return MoeRouteConfig(T, logits_stride, n_experts, top_k, n_groups, topk_groups, group_top, score, renormalise,
+                          logits_dtype, weight_scale, 0)
 
 
 def _p(v) -> int | None:
@@ -186,6 +218,25 @@ def moe_grouped_ffn(cfg, x_perm, offsets, w_gate_up, w_down, y_perm, ws, ws_byte
 def moe_combine(cfg, y_perm, row_of, topk_w, y_shared, y, stream=None) -> None:
     _check(lib().moe_combine(ctypes.byref(cfg), _p(y_perm), _p(row_of), _p(topk_w), _p(y_shared), _p(y),
                              _stream(stream)), "moe_combine")
+
+
+def moe_route_topk(route, logits, select_bias, topk_ids, topk_w, stream=None) -> None:
+    """Experts and routing weights of every row of ``logits`` (``route``: a MoeRouteConfig)."""
+    _check(lib().moe_route_topk(ctypes.byref(route), _p(logits), _p(select_bias), _p(topk_ids), _p(topk_w),
+                                _stream(stream)), "moe_route_topk")
+
+
+def moe_route_backward(route, logits, topk_ids, grad_w, counts, balance_coef, z_coef, grad_logits,
+                       stream=None) -> None:
+    """Gradient of the routing weights and of both penalties with respect to ``logits``."""
+    _check(lib().moe_route_backward(ctypes.byref(route), _p(logits), _p(topk_ids), _p(grad_w), _p(counts),
+                                    balance_coef, z_coef, _p(grad_logits), _stream(stream)), "moe_route_backward")
+
+
+def moe_combine_backward(cfg, grad_y, y_perm, row_of, topk_w, grad_y_perm, grad_w, stream=None) -> None:
+    """Gradients of moe_combine: of the experts' rows and of the routing weights (either may be None)."""
+    _check(lib().moe_combine_backward(ctypes.byref(cfg), _p(grad_y), _p(y_perm), _p(row_of), _p(topk_w),
+                                      _p(grad_y_perm), _p(grad_w), _stream(stream)), "moe_combine_backward")
 
 
 def moe_forward(cfg, x, w_router, logit_bias, w_gate_up, w_down, ws_gate_up, ws_down, y,

@@ -122,6 +122,48 @@ struct CombineArgs {
 };
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
 
+// ---- combine's gradient (combine_backward.cu)
+struct CombineBackwardArgs {
+  const void* grad_y;     // [T, d]
+  const void* y_perm;     // [T*k, d], or null without grad_w
+  const int32_t* row_of;  // [T*k]
+  const float* w;         // [T, k], or null without grad_y_perm
+  void* grad_y_perm;      // [T*k, d] or null
+  float* grad_w;          // [T, k] or null
+  int64_t T;
+  int k, d;
+  bool bf16;
+};
+cudaError_t launch_combine_backward(const CombineBackwardArgs& a, cudaStream_t stream);
+
+// ---- routing from logits (route.cu)
+struct RouteArgs {
+  const void* logits;     // [T, stride]
+  const float* bias;      // [E] or null
+  int32_t* ids;           // [T, k]
+  float* w;               // [T, k]
+  int64_t T, stride;
+  int E, k, G, Gk, group_top;
+  bool sigmoid, renorm, bf16;
+  float scale;
+  bool vec;               // set by the launcher: rows start on 16 bytes
+};
+cudaError_t launch_route_topk(const RouteArgs& a, cudaStream_t stream);
+struct RouteBackwardArgs {
+  const void* logits;     // [T, stride]
+  const int32_t* ids;     // [T, k], or null without grad_w
+  const float* grad_w;    // [T, k] or null
+  const int32_t* counts;  // [E], or null without a balance term
+  float balance, z;
+  void* grad;             // [T, stride]
+  int64_t T, stride;
+  int E, k;
+  bool sigmoid, renorm, bf16;
+  float scale;
+  bool vec;               // set by the launcher
+};
+cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t stream);
+
 int device_sm_count();
 int device_smem_per_block();  // opt-in dynamic shared memory per block (227 KiB on B200)
 

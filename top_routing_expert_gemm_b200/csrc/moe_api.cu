@@ -205,6 +205,33 @@ cudaError_t run_ffn(const moe_config* c, const Carve& k, const void* a, const in
   return launch_grouped_ffn_bf16_tc(g, s);
 }
 
+moe_status check_route_config(const moe_route_config* c) {
+  if (c == nullptr) return MOE_ERR_INVALID_ARG;
+  if (c->T < 0 || c->n_experts <= 0 || c->top_k <= 0 || c->n_groups <= 0 || c->reserved != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (c->logits_stride != 0 && c->logits_stride < c->n_experts) return MOE_ERR_INVALID_ARG;
+  if (c->n_experts % c->n_groups != 0 || c->topk_groups < 1 || c->topk_groups > c->n_groups)
+    return MOE_ERR_INVALID_ARG;
+  if ((int64_t)c->top_k > (int64_t)c->topk_groups * (c->n_experts / c->n_groups)) return MOE_ERR_INVALID_ARG;
+  if (c->group_top != 1 && c->group_top != 2) return MOE_ERR_INVALID_ARG;
+  if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (c->renormalise != 0 && c->renormalise != 1) return MOE_ERR_INVALID_ARG;
+  if (c->logits_dtype != MOE_F32 && c->logits_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(c->weight_scale)) return MOE_ERR_INVALID_ARG;
+  if (c->n_experts > kMaxExperts || c->top_k > kMaxTopK || c->n_groups > 32) return MOE_ERR_UNSUPPORTED;
+  const int64_t stride = c->logits_stride ? c->logits_stride : c->n_experts;
+  if (c->T >= (int64_t(1) << 31) / c->top_k || stride > (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int64_t route_stride(const moe_route_config* c) { return c->logits_stride ? c->logits_stride : c->n_experts; }
+
+RouteArgs route_args(const moe_route_config* c, const void* logits, const float* bias, int32_t* ids, float* w) {
+  return RouteArgs{logits, bias, ids, w, c->T, route_stride(c), c->n_experts, c->top_k, c->n_groups, c->topk_groups,
+                   c->group_top, c->score == MOE_SCORE_SIGMOID, c->renormalise != 0, c->logits_dtype == MOE_BF16,
+                   c->weight_scale, false};
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -341,6 +368,61 @@ moe_status moe_combine(const moe_config* cfg, const void* y_perm, const int32_t*
   if ((st = enter(g, y, stream)) != MOE_OK) return st;
   CombineArgs a{y_perm, row_of, topk_w, y_shared, y, cfg->T, cfg->top_k, cfg->d_model, cfg->dtype == MOE_BF16};
   MOE_CUDA_TRY(launch_combine(a, stream));
+  return MOE_OK;
+}
+
+moe_status moe_combine_backward(const moe_config* cfg, const void* grad_y, const void* y_perm,
+                                const int32_t* row_of, const float* topk_w, void* grad_y_perm, float* grad_w,
+                                moe_stream_t stream) {
+  moe_status st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (!grad_y_perm && !grad_w) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  if (!grad_y || !row_of || !aligned16(grad_y) || !aligned16(row_of) || (grad_w && !y_perm) ||
+      (grad_y_perm && !topk_w) || !aligned16(y_perm) || !aligned16(topk_w) || !aligned16(grad_y_perm) ||
+      !aligned16(grad_w))
+    return MOE_ERR_INVALID_ARG;
+  DeviceGuard g;
+  if ((st = enter(g, grad_y, stream)) != MOE_OK) return st;
+  CombineBackwardArgs a{grad_y, y_perm, row_of, topk_w, grad_y_perm, grad_w, cfg->T, cfg->top_k, cfg->d_model,
+                        cfg->dtype == MOE_BF16};
+  MOE_CUDA_TRY(launch_combine_backward(a, stream));
+  return MOE_OK;
+}
+
+moe_status moe_route_topk(const moe_route_config* cfg, const void* logits, const float* select_bias,
+                          int32_t* topk_ids, float* topk_w, moe_stream_t stream) {
+  moe_status st = check_route_config(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_w || !aligned16(logits) || !aligned16(topk_ids) || !aligned16(topk_w) ||
+      !aligned16(select_bias))
+    return MOE_ERR_INVALID_ARG;
+  DeviceGuard g;
+  if ((st = enter(g, topk_ids, stream)) != MOE_OK) return st;
+  if ((st = g.same_device(logits)) != MOE_OK) return st;
+  MOE_CUDA_TRY(launch_route_topk(route_args(cfg, logits, select_bias, topk_ids, topk_w), stream));
+  return MOE_OK;
+}
+
+moe_status moe_route_backward(const moe_route_config* cfg, const void* logits, const int32_t* topk_ids,
+                              const float* grad_w, const int32_t* counts, float balance_coef, float z_coef,
+                              void* grad_logits, moe_stream_t stream) {
+  moe_status st = check_route_config(cfg);
+  if (st != MOE_OK) return st;
+  if (!std::isfinite(balance_coef) || !std::isfinite(z_coef)) return MOE_ERR_INVALID_ARG;
+  if (balance_coef != 0.f && (!counts || !aligned16(counts))) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  if (!logits || !grad_logits || logits == grad_logits || !aligned16(logits) || !aligned16(grad_logits) ||
+      (grad_w && !topk_ids) || !aligned16(grad_w) || !aligned16(topk_ids))
+    return MOE_ERR_INVALID_ARG;
+  DeviceGuard g;
+  if ((st = enter(g, grad_logits, stream)) != MOE_OK) return st;
+  if ((st = g.same_device(logits)) != MOE_OK) return st;
+  RouteBackwardArgs a{logits, topk_ids, grad_w, counts, balance_coef, z_coef, grad_logits, cfg->T, route_stride(cfg),
+                      cfg->n_experts, cfg->top_k, cfg->score == MOE_SCORE_SIGMOID, cfg->renormalise != 0,
+                      cfg->logits_dtype == MOE_BF16, cfg->weight_scale, false};
+  MOE_CUDA_TRY(launch_route_backward(a, stream));
   return MOE_OK;
 }
 
