@@ -99,7 +99,8 @@ typedef enum {
   MOE_ERR_WORKSPACE = 3,    /* ws smaller than moe_workspace_bytes(cfg)       */
   MOE_ERR_CUDA = 4,         /* a CUDA runtime/driver call failed              */
   MOE_ERR_TIMEOUT = 5,      /* a bounded device wait expired (status word)    */
-  MOE_ERR_BAD_EXPERT_ID = 6 /* moe_permute saw an id outside [0, E) (status)  */
+  MOE_ERR_BAD_EXPERT_ID = 6, /* moe_permute saw an id outside [0, E) (status) */
+  MOE_ERR_BAD_ADAPTER_ID = 8 /* a token's adapter is not below n_adapters (status) */
 } moe_status;
 
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
@@ -411,8 +412,87 @@ moe_status moe_combine_backward(const moe_config* cfg, const void* grad_y, const
                                 const int32_t* row_of, const float* topk_w, void* grad_y_perm, float* grad_w,
                                 moe_stream_t stream);
 
-/* Synchronises `stream` and returns the status word of `ws`: MOE_OK,
-   MOE_ERR_TIMEOUT or MOE_ERR_BAD_EXPERT_ID (or MOE_ERR_CUDA). */
+/* ---------------------------------------------------------------- low-rank adapters
+   Adapters of many requests at once beside the expert projections, whose
+   weights all requests share: for a dispatched row of expert e whose token
+   uses adapter n
+     pre-activations  P + scale[n] * B[n,e] (A[n,e] x)       (gate_up)
+     outputs          y + scale[n] * B[n,e] (A[n,e] h)       (down)
+   A [N, E, r, inputs] and B [N, E, outputs, r] in the layer's dtype, scale [N]
+   fp32 (the usual alpha / r).  Beside a shared expert (shared = 1) the rows are
+   the tokens and each adapter has one A and one B (E = 1 in the shapes above,
+   d_ff_shared for d_ff).  Products accumulate in fp32; the adapter's term is
+   added to the base in fp32 and rounded once. */
+typedef struct {
+  int32_t n_adapters;       /* N, 1..65536                                     */
+  int32_t rank;             /* r, a multiple of 8, 8..128; an adapter of a
+                               lower rank is filled up with zeros              */
+  int32_t shared;           /* 0: the routed experts, 1: the shared expert     */
+  int32_t reserved;         /* 0                                               */
+} moe_adapter_config;
+
+/* Bytes of the plan of a batch: its first 16 bytes are a status word as in a
+   workspace (moe_device_status reads it); 0 on an invalid config. */
+size_t moe_adapter_plan_bytes(const moe_config* cfg, const moe_adapter_config* ad);
+
+/* Group the rows of a batch by (expert, adapter).  offsets [E+1] and perm as
+   moe_permute writes them (both NULL with shared = 1), token_adapter [T] int32:
+   a negative id is no adapter; an id from n_adapters on is treated so too and
+   flags MOE_ERR_BAD_ADAPTER_ID.  plan: 256-byte aligned scratch that the two
+   calls below read and use (it holds their partial sums), valid for as long as
+   the batch's rows are; calls that share a plan must not overlap.  Runs on the
+   device of plan. */
+moe_status moe_adapter_plan(const moe_config* cfg, const moe_adapter_config* ad, const int32_t* offsets,
+                            const int32_t* perm, const int32_t* token_adapter, void* plan, size_t plan_bytes,
+                            moe_stream_t stream);
+
+/* h[row] = act(pre[row] + scale[n] B[n,e] (A[n,e] x[row])), act the expert's
+   (moe_config.expert_act): x [rows, d], pre [rows, 2f] (gate, then up columns;
+   [rows, f] with MOE_ACT_GELU), a [N, E, r, d], b [N, E, 2f or f, r] -> h [rows, f].
+   Rows without an adapter get act(pre).  Rows behind offsets[E] are left as
+   they were.  h may be pre only with MOE_ACT_GELU. */
+moe_status moe_adapter_gate_up(const moe_config* cfg, const moe_adapter_config* ad, void* plan, size_t plan_bytes,
+                               const void* x, const void* a, const void* b, const float* scale, const void* pre,
+                               void* h, moe_stream_t stream);
+
+/* y[row] = base[row] + scale[n] B[n,e] (A[n,e] h[row]): h [rows, f], base
+   [rows, d], a [N, E, r, f], b [N, E, d, r] -> y [rows, d] (base itself, or
+   apart from it).  Rows without an adapter get base. */
+moe_status moe_adapter_down(const moe_config* cfg, const moe_adapter_config* ad, void* plan, size_t plan_bytes,
+                            const void* h, const void* a, const void* b, const float* scale, const void* base,
+                            void* y, moe_stream_t stream);
+
+/* Adapters of a layer call; a projection whose a and b are NULL has none (its
+   product then runs fused as in moe_forward). */
+typedef struct {
+  int32_t n_adapters, rank;       /* as moe_adapter_config; the same for all   */
+  const int32_t* token_adapter;   /* [T] int32                                 */
+  const float* scale;             /* [N] fp32                                  */
+  const void *a_gate_up, *b_gate_up, *a_down, *b_down;             /* routed experts */
+  const void *a_gate_up_shared, *b_gate_up_shared, *a_down_shared, *b_down_shared;
+} moe_adapters;
+
+/* Bytes of workspace of moe_forward_routed (adapters may be NULL); 0 on an
+   invalid config. */
+size_t moe_forward_routed_workspace_bytes(const moe_config* cfg, const moe_adapters* adapters);
+
+/* The layer from router logits: moe_route_topk -> dispatch -> experts with the
+   requests' adapters (NULL: none) -> combine.  route's T, n_experts and top_k
+   are cfg's; cfg's gating and bias_select_only are not used.  Tokens whose
+   slots are empty (id -1) reach no routed expert; a batch padded to a fixed
+   size masks its padding's logits.  With gate_up adapters the pre-activations
+   are stored in dtype between the first product and the adapters' kernel.
+   Otherwise as moe_forward (optional outputs, status word, launches); a bad
+   adapter id flags MOE_ERR_BAD_ADAPTER_ID in the status word of ws. */
+moe_status moe_forward_routed(const moe_config* cfg, const moe_route_config* route, const moe_adapters* adapters,
+                              const void* x, const void* logits, const float* select_bias, const void* w_gate_up,
+                              const void* w_down, const void* ws_gate_up, const void* ws_down, void* y,
+                              int32_t* opt_topk_ids, float* opt_topk_w, int32_t* opt_counts, void* ws,
+                              size_t ws_bytes, moe_stream_t stream);
+
+/* Synchronises `stream` and returns the status word of `ws` (or of an adapter
+   plan): MOE_OK, MOE_ERR_TIMEOUT, MOE_ERR_BAD_EXPERT_ID or
+   MOE_ERR_BAD_ADAPTER_ID (or MOE_ERR_CUDA). */
 moe_status moe_device_status(const void* ws, size_t ws_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus

@@ -100,3 +100,99 @@ def test_injected_launch_failure(L, monkeypatch):
     assert _topk(L, _route()) == CUDA and _back(L, _route()) == CUDA
     assert L.moe_combine_backward(ctypes.byref(cfg), _p(), _p(), _p(), _p(), _p(), _p(), None) == CUDA
     assert _topk(L, _route(top_k=0)) == INVALID
+
+
+# ------------------------------------------------------------------ adapters
+def _plan(L, cfg, ad, offsets=256, perm=256, ta=256, plan=256, nb=1 << 40):
+    return L.moe_adapter_plan(ctypes.byref(cfg), ctypes.byref(ad) if ad else None, _p(offsets), _p(perm), _p(ta),
+                              _p(plan), nb, None)
+
+
+def _apply(L, cfg, ad, which="down", plan=256, nb=1 << 40, x=256, a=256, b=256, scale=256, base=256, out=512):
+    f = L.moe_adapter_gate_up if which == "gate_up" else L.moe_adapter_down
+    return f(ctypes.byref(cfg), ctypes.byref(ad) if ad else None, _p(plan), nb, _p(x), _p(a), _p(b), _p(scale),
+             _p(base), _p(out), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n_adapters=0, rank=8), INVALID), (dict(n_adapters=-1, rank=8), INVALID), (dict(n_adapters=2, rank=0), INVALID),
+    (dict(n_adapters=2, rank=12), INVALID), (dict(n_adapters=2, rank=8, shared=2), INVALID),
+    (dict(n_adapters=2, rank=8, shared=1), INVALID),  # the layer has no shared expert
+    (dict(n_adapters=2, rank=136), UNSUPPORTED), (dict(n_adapters=65537, rank=8), UNSUPPORTED),
+])
+def test_adapter_config_refusals(L, kw, want):
+    ad = moe.make_adapter_config(**kw)
+    assert moe.moe_adapter_plan_bytes(_cfg(), ad) == 0
+    assert _plan(L, _cfg(), ad) == want and _apply(L, _cfg(), ad) == want and _apply(L, _cfg(), ad, "gate_up") == want
+
+
+def test_adapter_argument_refusals(L):
+    cfg, ad = _cfg(), moe.make_adapter_config(3, 16)
+    need = moe.moe_adapter_plan_bytes(cfg, ad)
+    assert need > 0 and need % 256 == 0
+    assert _plan(L, cfg, None) == INVALID and _apply(L, cfg, None) == INVALID
+    assert _plan(L, _cfg(top_k=9), ad) == INVALID
+    for name in ("offsets", "perm", "ta", "plan"):
+        assert _plan(L, cfg, ad, **{name: None}) == INVALID
+        assert _plan(L, cfg, ad, **{name: 264}) == INVALID
+    assert _plan(L, cfg, ad, plan=16) == INVALID               # 256-byte alignment
+    assert _plan(L, cfg, ad, nb=need - 1) == WORKSPACE and _apply(L, cfg, ad, nb=need - 1) == WORKSPACE
+    sh = _cfg(n_shared=1, d_ff_shared=512)
+    assert _plan(L, sh, moe.make_adapter_config(3, 16, 1)) == INVALID   # a shared expert has no dispatch
+    for which in ("gate_up", "down"):
+        for name in ("plan", "x", "a", "b", "scale", "base", "out"):
+            assert _apply(L, cfg, ad, which, **{name: None}) == INVALID
+            assert _apply(L, cfg, ad, which, **{name: 264}) == INVALID
+        assert _apply(L, cfg, ad, which, x=512) == INVALID     # the result over the input
+    assert _apply(L, cfg, ad, "gate_up", base=512) == INVALID  # SwiGLU halves the columns: not in place
+    assert _apply(L, _cfg(T=0), ad, x=None, a=None, plan=None) == 0
+
+
+def _forward(L, cfg, rc, ad, ws=256, nb=1 << 40, x=256, logits=256, wgu=256, wd=256, sgu=None, sd=None, y=256):
+    return L.moe_forward_routed(ctypes.byref(cfg), ctypes.byref(rc), ctypes.byref(ad) if ad else None, _p(x),
+                                _p(logits), None, _p(wgu), _p(wd), _p(sgu), _p(sd), _p(y), None, None, None, _p(ws),
+                                nb, None)
+
+
+def _layer_route(cfg, **kw):
+    return moe.make_route_config(cfg.T, cfg.n_experts, cfg.top_k, moe.MOE_SCORE_SOFTMAX, **kw)
+
+
+def test_forward_routed_refusals(L):
+    cfg = _cfg()
+    rc = _layer_route(cfg)
+    need = moe.moe_forward_routed_workspace_bytes(cfg)
+    assert need == moe.moe_workspace_bytes(cfg)
+    assert _forward(L, cfg, rc, None, nb=need - 1) == WORKSPACE
+    for bad in (dict(T=63), dict(n_experts=16), dict(top_k=3)):
+        assert _forward(L, cfg, _layer_route(_cfg(**bad)), None) == INVALID
+    for name in ("ws", "x", "logits", "wgu", "wd", "y"):
+        assert _forward(L, cfg, rc, None, **{name: None}) == INVALID
+        assert _forward(L, cfg, rc, None, **{name: 264}) == INVALID
+    assert _forward(L, _cfg(n_shared=1, d_ff_shared=512), rc, None) == INVALID  # shared weights missing
+    p = 256
+    ad = moe.make_adapters(4, 16, p, p, p, p, p, p)
+    more = moe.moe_forward_routed_workspace_bytes(cfg, ad)
+    assert more > need + 128 * 2 * 512 * 2                     # the pre-activations
+    assert _forward(L, cfg, rc, ad, nb=more - 1) == WORKSPACE
+    assert moe.moe_forward_routed_workspace_bytes(cfg, moe.make_adapters(4, 16, p, p, a_down=p, b_down=p)) < more
+    for bad in (moe.make_adapters(4, 16, None, p, p, p), moe.make_adapters(4, 16, p, None, p, p),
+                moe.make_adapters(4, 16, p, p, p, None), moe.make_adapters(4, 16, p, p, b_down=p),
+                moe.make_adapters(4, 12, p, p, p, p), moe.make_adapters(4, 16, p, p, 264, p),
+                moe.make_adapters(4, 16, p, p, a_down_shared=p, b_down_shared=p)):
+        assert moe.moe_forward_routed_workspace_bytes(cfg, bad) == 0
+        assert _forward(L, cfg, rc, bad) == INVALID
+
+
+def test_injected_launch_failure_of_the_adapter_calls(L, monkeypatch):
+    monkeypatch.setenv("MOE_FAULT", "launch")
+    cfg, ad = _cfg(), moe.make_adapter_config(3, 16)
+    assert _plan(L, cfg, ad) == CUDA and _apply(L, cfg, ad) == CUDA and _apply(L, cfg, ad, "gate_up") == CUDA
+    assert _forward(L, cfg, _layer_route(cfg), None) == CUDA
+    assert _plan(L, cfg, ad, nb=16) == WORKSPACE
+
+
+def test_adapter_struct_layouts():
+    assert ctypes.sizeof(moe.MoeAdapterConfig) == 16
+    assert ctypes.sizeof(moe.MoeAdapters) == 88 and moe.MoeAdapters.a_gate_up.offset == 24
+    assert moe.moe_status_string(8) == "adapter id out of range"

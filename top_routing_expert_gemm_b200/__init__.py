@@ -18,7 +18,9 @@ __all__ = [
     "MOE_F32", "MOE_BF16", "MOE_SOFTMAX_ALL_RENORM", "MOE_SOFTMAX_TOPK", "MOE_SIGMOID_TOPK_RENORM",
     "MOE_SOFTMAX_ALL_NO_RENORM", "MOE_ACT_SWIGLU", "MOE_ACT_GELU",
     "MoeRouteConfig", "make_route_config", "moe_route_topk", "moe_route_backward", "moe_combine_backward",
-    "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID",
+    "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MoeAdapterConfig", "MoeAdapters", "make_adapter_config",
+    "make_adapters", "moe_adapter_plan_bytes", "moe_adapter_plan", "moe_adapter_gate_up", "moe_adapter_down",
+    "moe_forward_routed", "moe_forward_routed_workspace_bytes",
     "EXPORTED_SYMBOLS", "LIB_PATH",
 ]
 
@@ -27,6 +29,7 @@ LIB_PATH = pathlib.Path(__file__).resolve().parent / "libmoe_b200.so"
 MOE_OK = 0
 MOE_ERR_TIMEOUT = 5
 MOE_ERR_BAD_EXPERT_ID = 6
+MOE_ERR_BAD_ADAPTER_ID = 8
 MOE_F32, MOE_BF16 = 0, 1
 MOE_SOFTMAX_ALL_RENORM, MOE_SOFTMAX_TOPK, MOE_SIGMOID_TOPK_RENORM, MOE_SOFTMAX_ALL_NO_RENORM = 0, 1, 2, 3
 MOE_ACT_SWIGLU, MOE_ACT_GELU = 0, 1
@@ -37,7 +40,8 @@ EXPORTED_SYMBOLS = (
     "moe_workspace_bytes", "moe_status_string", "moe_router_topk", "moe_permute", "moe_grouped_ffn",
     "moe_combine", "moe_forward", "moe_device_status", "moe_permute_noalloc", "moe_expert_capacity",
     "moe_router_aux_losses", "moe_e4m3_weight_bytes", "moe_quantize_e4m3", "moe_forward_traced",
-    "moe_route_topk", "moe_route_backward", "moe_combine_backward",
+    "moe_route_topk", "moe_route_backward", "moe_combine_backward", "moe_adapter_plan_bytes", "moe_adapter_plan",
+    "moe_adapter_gate_up", "moe_adapter_down", "moe_forward_routed", "moe_forward_routed_workspace_bytes",
 )
 
 
@@ -83,6 +87,32 @@ class MoeRouteConfig(ctypes.Structure):
     ]
 
 
+class MoeAdapterConfig(ctypes.Structure):
+    _fields_ = [
+        ("n_adapters", ctypes.c_int32),
+        ("rank", ctypes.c_int32),
+        ("shared", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class MoeAdapters(ctypes.Structure):
+    _fields_ = [
+        ("n_adapters", ctypes.c_int32),
+        ("rank", ctypes.c_int32),
+        ("token_adapter", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("a_gate_up", ctypes.c_void_p),
+        ("b_gate_up", ctypes.c_void_p),
+        ("a_down", ctypes.c_void_p),
+        ("b_down", ctypes.c_void_p),
+        ("a_gate_up_shared", ctypes.c_void_p),
+        ("b_gate_up_shared", ctypes.c_void_p),
+        ("a_down_shared", ctypes.c_void_p),
+        ("b_down_shared", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -116,8 +146,17 @@ def lib() -> ctypes.CDLL:
         L.moe_route_topk.argtypes = [rcp, vp, vp, vp, vp, vp]
         L.moe_route_backward.argtypes = [rcp, vp, vp, vp, vp, f32, f32, vp, vp]
         L.moe_combine_backward.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp]
+        adp = ctypes.POINTER(MoeAdapterConfig)
+        L.moe_adapter_plan_bytes.argtypes = [cfgp, adp]
+        L.moe_adapter_plan.argtypes = [cfgp, adp, vp, vp, vp, vp, sz, vp]
+        L.moe_adapter_gate_up.argtypes = [cfgp, adp, vp, sz, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_adapter_down.argtypes = [cfgp, adp, vp, sz, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_forward_routed_workspace_bytes.argtypes = [cfgp, ctypes.POINTER(MoeAdapters)]
+        L.moe_forward_routed.argtypes = [cfgp, rcp, ctypes.POINTER(MoeAdapters)] + [vp] * 12 + [sz, vp]
         for name in EXPORTED_SYMBOLS[2:]:
             getattr(L, name).restype = i32
+        L.moe_adapter_plan_bytes.restype = sz
+        L.moe_forward_routed_workspace_bytes.restype = sz
         L.moe_expert_capacity.restype = ctypes.c_int64
         L.moe_e4m3_weight_bytes.restype = sz
         _lib = L
@@ -137,6 +176,20 @@ def make_route_config(T: int, n_experts: int, top_k: int, score: int, n_groups: 
                       logits_dtype: int = MOE_F32, logits_stride: int = 0) -> MoeRouteConfig:
     return MoeRouteConfig(T, logits_stride, n_experts, top_k, n_groups, topk_groups, group_top, score, renormalise,
                           logits_dtype, weight_scale, 0)
+
+
+def make_adapter_config(n_adapters: int, rank: int, shared: int = 0) -> MoeAdapterConfig:
+    return MoeAdapterConfig(n_adapters, rank, shared, 0)
+
+
+def make_adapters(n_adapters: int, rank: int, token_adapter, scale, a_gate_up=None, b_gate_up=None, a_down=None,
+                  b_down=None, a_gate_up_shared=None, b_gate_up_shared=None, a_down_shared=None,
+                  b_down_shared=None) -> MoeAdapters:
+    """The adapters of a layer call.  Holds device addresses only: the tensors
+    must outlive it."""
+    return MoeAdapters(n_adapters, rank, *map(_p, (token_adapter, scale, a_gate_up, b_gate_up, a_down, b_down,
+                                                   a_gate_up_shared, b_gate_up_shared, a_down_shared,
+                                                   b_down_shared)))
 
 
 def _p(v) -> int | None:
@@ -237,6 +290,48 @@ def moe_combine_backward(cfg, grad_y, y_perm, row_of, topk_w, grad_y_perm, grad_
     """Gradients of moe_combine: of the experts' rows and of the routing weights (either may be None)."""
     _check(lib().moe_combine_backward(ctypes.byref(cfg), _p(grad_y), _p(y_perm), _p(row_of), _p(topk_w),
                                       _p(grad_y_perm), _p(grad_w), _stream(stream)), "moe_combine_backward")
+
+
+def moe_adapter_plan_bytes(cfg, adapters) -> int:
+    return int(lib().moe_adapter_plan_bytes(ctypes.byref(cfg), ctypes.byref(adapters)))
+
+
+def moe_adapter_plan(cfg, adapters, offsets, perm, token_adapter, plan, plan_bytes=None, stream=None) -> None:
+    """Group a batch's rows by (expert, adapter) into ``plan`` (``adapters``: a MoeAdapterConfig)."""
+    nb = plan_bytes if plan_bytes is not None else plan.numel() * plan.element_size()
+    _check(lib().moe_adapter_plan(ctypes.byref(cfg), ctypes.byref(adapters), _p(offsets), _p(perm),
+                                  _p(token_adapter), _p(plan), nb, _stream(stream)), "moe_adapter_plan")
+
+
+def moe_adapter_gate_up(cfg, adapters, plan, x, a, b, scale, pre, h, plan_bytes=None, stream=None) -> None:
+    """h = act(pre + scale B A x) for every row of the plan."""
+    nb = plan_bytes if plan_bytes is not None else plan.numel() * plan.element_size()
+    _check(lib().moe_adapter_gate_up(ctypes.byref(cfg), ctypes.byref(adapters), _p(plan), nb, _p(x), _p(a), _p(b),
+                                     _p(scale), _p(pre), _p(h), _stream(stream)), "moe_adapter_gate_up")
+
+
+def moe_adapter_down(cfg, adapters, plan, h, a, b, scale, base, y, plan_bytes=None, stream=None) -> None:
+    """y = base + scale B A h for every row of the plan."""
+    nb = plan_bytes if plan_bytes is not None else plan.numel() * plan.element_size()
+    _check(lib().moe_adapter_down(ctypes.byref(cfg), ctypes.byref(adapters), _p(plan), nb, _p(h), _p(a), _p(b),
+                                  _p(scale), _p(base), _p(y), _stream(stream)), "moe_adapter_down")
+
+
+def moe_forward_routed_workspace_bytes(cfg, adapters=None) -> int:
+    return int(lib().moe_forward_routed_workspace_bytes(ctypes.byref(cfg),
+                                                        ctypes.byref(adapters) if adapters is not None else None))
+
+
+def moe_forward_routed(cfg, route, adapters, x, logits, select_bias, w_gate_up, w_down, ws_gate_up, ws_down, y,
+                       opt_topk_ids=None, opt_topk_w=None, opt_counts=None, ws=None, ws_bytes=None,
+                       stream=None) -> None:
+    """The layer from router logits, with the requests' adapters (a MoeAdapters or None)."""
+    nb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(lib().moe_forward_routed(ctypes.byref(cfg), ctypes.byref(route),
+                                    ctypes.byref(adapters) if adapters is not None else None, _p(x), _p(logits),
+                                    _p(select_bias), _p(w_gate_up), _p(w_down), _p(ws_gate_up), _p(ws_down), _p(y),
+                                    _p(opt_topk_ids), _p(opt_topk_w), _p(opt_counts), _p(ws), nb, _stream(stream)),
+           "moe_forward_routed")
 
 
 def moe_forward(cfg, x, w_router, logit_bias, w_gate_up, w_down, ws_gate_up, ws_down, y,

@@ -11,6 +11,7 @@ namespace moe {
 // status word values written by kernels (mirrors moe_status in include/moe.h)
 constexpr int kDevTimeout = 5;
 constexpr int kDevBadExpertId = 6;
+constexpr int kDevBadAdapterId = 8;
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 16;

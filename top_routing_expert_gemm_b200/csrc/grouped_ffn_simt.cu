@@ -133,14 +133,24 @@ cudaError_t launch_grouped_ffn_f32_simt(const GroupedFfnArgs& a, cudaStream_t st
   if (a.rows == 0) return cudaSuccess;
   const int64_t mt_bound = (a.rows + BM - 1) / BM + (a.offsets ? a.G : 0);
   const dim3 grid1((unsigned)mt_bound, (unsigned)((a.f + BN - 1) / BN));
-  if (a.act == kEpiGELU)
+  if (a.part == kFfnGemm2) {
+    // h is given
+  } else if (a.part == kFfnGemm1Plain) {  // without the activation: the columns of [gate; up] (or up)
+    const int cols = a.act == kEpiGELU ? a.f : 2 * a.f;
+    grouped_gemm_f32_kernel<kEpiNone><<<dim3((unsigned)mt_bound, (unsigned)((cols + BN - 1) / BN)), kThreads, 0,
+                                        stream>>>(
+        static_cast<const float*>(a.a), a.rows, a.offsets, a.G, static_cast<const float*>(a.w_gate_up),
+        (int64_t)cols, 0, a.d, cols, static_cast<float*>(a.h));
+  } else if (a.act == kEpiGELU) {
     grouped_gemm_f32_kernel<kEpiGELU><<<grid1, kThreads, 0, stream>>>(
         static_cast<const float*>(a.a), a.rows, a.offsets, a.G, static_cast<const float*>(a.w_gate_up),
         (int64_t)a.f, 0, a.d, a.f, static_cast<float*>(a.h));
-  else
+  } else {
     grouped_gemm_f32_kernel<kEpiSwiGLU><<<grid1, kThreads, 0, stream>>>(
         static_cast<const float*>(a.a), a.rows, a.offsets, a.G, static_cast<const float*>(a.w_gate_up),
         2 * (int64_t)a.f, a.f, a.d, a.f, static_cast<float*>(a.h));
+  }
+  if (a.part == kFfnGemm1 || a.part == kFfnGemm1Plain) return cudaGetLastError();
   const dim3 grid2((unsigned)mt_bound, (unsigned)((a.d + BN - 1) / BN));
   grouped_gemm_f32_kernel<kEpiNone><<<grid2, kThreads, 0, stream>>>(
       static_cast<const float*>(a.h), a.rows, a.offsets, a.G, static_cast<const float*>(a.w_down), a.d, 0, a.f,

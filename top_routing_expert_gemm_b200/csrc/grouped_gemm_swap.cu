@@ -538,7 +538,9 @@ cudaError_t run_swap(const GroupedFfnArgs& a, cudaStream_t stream) {
   const int sms = device_sm_count();
   const int eb = FP8 ? 1 : 2;
   const bool gelu = a.act == kEpiGELU;
-  const int J1 = gelu ? (a.f + 127) / 128 : (a.f + 63) / 64, J2 = (a.d + 127) / 128;
+  const bool plain = a.part == kFfnGemm1Plain;  // GEMM-1 without its activation: blocks of 128 rows of [gate; up]
+  const int n1 = plain && !gelu ? 2 * a.f : a.f;
+  const int J1 = gelu || plain ? (n1 + 127) / 128 : (a.f + 63) / 64, J2 = (a.d + 127) / 128;
   const int64_t cap1 = unit_bound(a.rows, G, BN, J1), cap2 = unit_bound(a.rows, G, BN, J2);
   if (cap1 > a.counter_cap || cap2 > a.counter_cap) return cudaErrorInvalidValue;
   const int grid = std::max(1, std::min(sms, kDecodeMaxCtas));
@@ -548,15 +550,19 @@ cudaError_t run_swap(const GroupedFfnArgs& a, cudaStream_t stream) {
   const float* s1 = FP8 ? reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.w_gate_up) +
                                                          e4m3_codes_bytes((int64_t)a.G * w1_rows, a.d))
                         : nullptr;
-  CUtensorMap w1, x1a, x1b;
-  if (!make_map(&w1, a.w_gate_up, (uint64_t)a.G * w1_rows, a.d, gelu ? S_BM : 64, eb) ||
-      !make_map(&x1a, a.a, a.rows, a.d, 64, eb) || !make_map(&x1b, a.a, a.rows, a.d, 16, eb))
-    return cudaErrorInvalidValue;
-  SwapParams p1{a.offsets, G, a.rows, a.d, a.f, J1, w1_rows, a.f, static_cast<__nv_bfloat16*>(a.h), a.f,
-                a.partial, a.counters, a.counter_cap, a.status, lim, a.sa, s1};
-  cudaError_t e = gelu ? launch_swap<kEpiGELU, FP8>(w1, x1a, x1b, p1, grid, a.chained, stream)
-                       : launch_swap<kEpiSwiGLU, FP8>(w1, x1a, x1b, p1, grid, a.chained, stream);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (a.part != kFfnGemm2) {
+    CUtensorMap w1, x1a, x1b;
+    if (!make_map(&w1, a.w_gate_up, (uint64_t)a.G * w1_rows, a.d, gelu || plain ? S_BM : 64, eb) ||
+        !make_map(&x1a, a.a, a.rows, a.d, 64, eb) || !make_map(&x1b, a.a, a.rows, a.d, 16, eb))
+      return cudaErrorInvalidValue;
+    SwapParams p1{a.offsets, G, a.rows, a.d, n1, J1, w1_rows, a.f, static_cast<__nv_bfloat16*>(a.h), n1,
+                  a.partial, a.counters, a.counter_cap, a.status, lim, a.sa, s1};
+    e = plain  ? launch_swap<kEpiNone, FP8>(w1, x1a, x1b, p1, grid, a.chained, stream)
+        : gelu ? launch_swap<kEpiGELU, FP8>(w1, x1a, x1b, p1, grid, a.chained, stream)
+               : launch_swap<kEpiSwiGLU, FP8>(w1, x1a, x1b, p1, grid, a.chained, stream);
+    if (e != cudaSuccess || a.part == kFfnGemm1 || plain) return e;
+  }
   const void* b2 = a.h;
   const float* sx2 = nullptr;
   if (FP8) {  // h -> E4M3 codes and per-token scales

@@ -664,15 +664,27 @@ cudaError_t run_tc(const GroupedFfnArgs& a, cudaStream_t stream) {
                                                          e4m3_codes_bytes(w1_rows, a.d))
                         : nullptr;
   CUtensorMap mA1, mB1;
-  cudaError_t e;
+  cudaError_t e = cudaSuccess;
   // 8-bit: GEMM-1's epilogue leaves each row's largest |h| in sh (as bf16
   // bits), so the re-quantisation of h reads h once
-  uint32_t* row_amax = FP8 ? reinterpret_cast<uint32_t*>(a.sh) : nullptr;
-  if (FP8) {
+  uint32_t* row_amax = FP8 && a.part == kFfnBoth ? reinterpret_cast<uint32_t*>(a.sh) : nullptr;
+  if (row_amax) {
     e = cudaMemsetAsync(a.sh, 0, sizeof(float) * (size_t)a.rows, stream);
     if (e != cudaSuccess) return e;
   }
-  if (gelu) {
+  if (a.part == kFfnGemm2) {
+    // h is given
+  } else if (a.part == kFfnGemm1Plain) {
+    // GEMM-1 without its activation: tile = 128 rows x n columns of [gate; up] (or up)
+    const int cols = gelu ? a.f : 2 * a.f;
+    const bool deep = deep_ring(cols, false, FP8, G);
+    const int n = deep ? 224 : BN_MMA;
+    if (!make_map(&mA1, a.a, a.rows, a.d, BM, eb) || !make_map(&mB1, a.w_gate_up, w1_rows, a.d, n, eb))
+      return cudaErrorInvalidValue;
+    Params p1{a.offsets, G, a.rows, a.d, cols, (cols + n - 1) / n, (int64_t)cols, 0, a.h, cols, a.status, lim, n,
+              a.sa, s1};
+    e = launch_ffn<MODE_PLAIN, FP8>(deep, mA1, mB1, p1, mt_bound * p1.nt, stream);
+  } else if (gelu) {
     // GEMM-1 + GELU: tile = 128 rows x n1 up columns
     if (!make_map(&mA1, a.a, a.rows, a.d, BM, eb) || !make_map(&mB1, a.w_gate_up, w1_rows, a.d, n1, eb))
       return cudaErrorInvalidValue;
@@ -689,7 +701,7 @@ cudaError_t run_tc(const GroupedFfnArgs& a, cudaStream_t stream) {
     p1.row_amax = row_amax;
     e = launch_ffn<MODE_SWIGLU, FP8>(deep1, mA1, mB1, p1, mt_bound * p1.nt, stream);
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.part == kFfnGemm1 || a.part == kFfnGemm1Plain) return e;
   const void* a2 = a.h;
   const float* sa2 = nullptr;
   if (FP8) {  // h -> E4M3 codes and per-token scales

@@ -50,6 +50,7 @@ struct PermuteArgs {
   int* status;
   int64_t capacity;       // rows each expert keeps (n_assign or more: dropless)
   bool chained;           // the dispatch kernels may be launched programmatically (pdl.cuh)
+  int min_id;             // ids below it (and from E on) are reported: 0, or -1 where -1 means an empty slot
 };
 int permute_n_chunks(int64_t n_assign);
 cudaError_t launch_permute(const PermuteArgs& a, cudaStream_t stream);
@@ -85,7 +86,12 @@ struct GroupedFfnArgs {
   // decode kernel: the counters were zeroed ahead of this call, so GEMM-1 is
   // launched programmatically after its predecessor (pdl.cuh) with no clearing
   bool chained;
+  // which of the two products to run: both, or one of them where adapters
+  // work between; kFfnGemm1Plain leaves the activation out (h then takes the
+  // pre-activations [rows, 2f] or [rows, f])
+  int part;
 };
+constexpr int kFfnBoth = 0, kFfnGemm1 = 1, kFfnGemm1Plain = 2, kFfnGemm2 = 3;
 constexpr int kDecodeMaxCtas = 160;  // CTAs of one decode-schedule launch, at most
 constexpr int kDecodeTokens = 64;    // most tokens per unit of the decode schedule
 cudaError_t launch_grouped_ffn_bf16_tc(const GroupedFfnArgs& a, cudaStream_t stream);      // tcgen05, token rows as M
@@ -163,6 +169,35 @@ struct RouteBackwardArgs {
   bool vec;               // set by the launcher
 };
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t stream);
+
+// ---- low-rank adapters beside the experts' projections (adapter.cu)
+struct AdapterShape {
+  int64_t T, rows;        // tokens; dispatched rows (T*k, or T beside a shared expert)
+  int d, f;               // inputs of the two projections
+  int E, k;               // experts per adapter; rows per token (1, 1 beside a shared expert)
+  int N, r;               // adapters, rank
+  int act;                // kEpiSwiGLU or kEpiGELU
+  bool bf16;
+};
+struct AdapterApply {
+  bool gate_up;           // the first projection (d -> 2f or f, activation -> f), else the second (f -> d)
+  const void* x;          // [rows, d or f]
+  const void* a;          // [N, E, r, inputs]
+  const void* b;          // [N, E, outputs, r]
+  const float* scale;     // [N]
+  const void* base;       // [rows, outputs]
+  void* out;              // [rows, f or d]
+  void* plan;
+};
+constexpr size_t kAdapterTilesAt = 64;  // byte offset of the tile count in the plan's header
+size_t adapter_plan_bytes(const AdapterShape& s);
+// The plan's header (kAdapterHeader bytes) has to be zero; status: where a bad
+// adapter id is reported (the header's first word, or a workspace's).
+constexpr size_t kAdapterHeader = 256;
+cudaError_t launch_adapter_plan(const AdapterShape& s, const int32_t* offsets, const int32_t* perm,
+                                const int32_t* token_adapter, void* plan, int* status, bool chained,
+                                cudaStream_t stream);
+cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, bool chained, cudaStream_t stream);
 
 int device_sm_count();
 int device_smem_per_block();  // opt-in dynamic shared memory per block (227 KiB on B200)

@@ -182,16 +182,16 @@ moe_status enter(DeviceGuard& g, const void* p, cudaStream_t stream) {
 // launches (pdl.cuh)
 cudaError_t run_ffn(const moe_config* c, const Carve& k, const void* a, const int32_t* offsets, int G, int64_t rows,
                     int f, const void* w_gu, const void* w_d, void* h, void* y, cudaStream_t s, bool shared = false,
-                    bool a_quantized = false, bool chained = false) {
+                    bool a_quantized = false, bool chained = false, int part = kFfnBoth) {
   GroupedFfnArgs g{a, offsets, w_gu, w_d, h, y, rows, G, c->d_model, f, c->expert_act, k.status, wait_limit(c),
                    false, nullptr, nullptr, nullptr, k.partial, k.partial_slots, k.counters, k.counter_cap,
-                   chained};
+                   chained, part};
   if (c->dtype != MOE_BF16) return launch_grouped_ffn_f32_simt(g, s);
   if (c->weight_format == MOE_W_E4M3) {
     // the expert input -> E4M3 codes and per-token scales (only the rows in use)
     uint8_t* xq = shared ? k.xq_s : k.xq;
     float* sx = shared ? k.sx_s : k.sx;
-    if (!a_quantized) {
+    if (!a_quantized && part != kFfnGemm2) {
       const cudaError_t e = launch_quantize_e4m3(a, rows, offsets ? offsets + G : nullptr, c->d_model, xq, sx, s);
       if (e != cudaSuccess) return e;
     }
@@ -230,6 +230,120 @@ RouteArgs route_args(const moe_route_config* c, const void* logits, const float*
   return RouteArgs{logits, bias, ids, w, c->T, route_stride(c), c->n_experts, c->top_k, c->n_groups, c->topk_groups,
                    c->group_top, c->score == MOE_SCORE_SIGMOID, c->renormalise != 0, c->logits_dtype == MOE_BF16,
                    c->weight_scale, false};
+}
+
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) % kAlign) == 0; }
+
+moe_status check_adapter_config(const moe_config* c, const moe_adapter_config* ad) {
+  const moe_status st = check_config(c);
+  if (st != MOE_OK) return st;
+  if (ad == nullptr || ad->n_adapters <= 0 || ad->rank <= 0 || ad->rank % 8 != 0 || ad->reserved != 0 ||
+      (ad->shared != 0 && ad->shared != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (ad->shared && c->n_shared == 0) return MOE_ERR_INVALID_ARG;
+  if (ad->n_adapters > 65536 || ad->rank > 128) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+AdapterShape adapter_shape(const moe_config* c, int N, int r, bool shared) {
+  const int act = c->expert_act == MOE_ACT_GELU ? kEpiGELU : kEpiSwiGLU;
+  return AdapterShape{c->T, shared ? c->T : c->T * c->top_k, c->d_model, shared ? c->d_ff_shared : c->d_ff,
+                      shared ? 1 : c->n_experts, shared ? 1 : c->top_k, N, r, act, c->dtype == MOE_BF16};
+}
+
+moe_status adapter_apply(const moe_config* cfg, const moe_adapter_config* ad, bool gate_up, void* plan,
+                         size_t plan_bytes, const void* x, const void* a, const void* b, const float* scale,
+                         const void* base, void* out, cudaStream_t stream) {
+  moe_status st = check_adapter_config(cfg, ad);
+  if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  const AdapterShape s = adapter_shape(cfg, ad->n_adapters, ad->rank, ad->shared != 0);
+  if (!plan || !aligned256(plan)) return MOE_ERR_INVALID_ARG;
+  if (plan_bytes < adapter_plan_bytes(s)) return MOE_ERR_WORKSPACE;
+  if (!x || !a || !b || !scale || !base || !out || !aligned16(x) || !aligned16(a) || !aligned16(b) ||
+      !aligned16(scale) || !aligned16(base) || !aligned16(out) || x == out)
+    return MOE_ERR_INVALID_ARG;
+  if (gate_up && base == out && cfg->expert_act != MOE_ACT_GELU) return MOE_ERR_INVALID_ARG;
+  DeviceGuard g;
+  if ((st = enter(g, plan, stream)) != MOE_OK) return st;
+  if ((st = g.same_device(out)) != MOE_OK) return st;
+  MOE_CUDA_TRY(launch_adapter_apply(s, AdapterApply{gate_up, x, a, b, scale, base, out, plan}, false, stream));
+  return MOE_OK;
+}
+
+// What a layer call with adapters needs beyond moe_workspace_bytes: the
+// pre-activations and the plan of the routed and of the shared experts, and
+// the dispatched rows themselves where 8-bit experts keep only their codes.
+struct RoutedCarve {
+  void *pre, *pre_s, *plan, *plan_s, *x_perm;
+  size_t total;
+};
+RoutedCarve carve_routed(const moe_config* c, const moe_adapters* ad, void* base) {
+  RoutedCarve k{};
+  uint8_t* b = static_cast<uint8_t*>(base);
+  size_t off = carve(c, nullptr).total;
+  auto take = [&](size_t bytes) -> void* {
+    void* p = b ? b + off : nullptr;
+    off += up(bytes);
+    return p;
+  };
+  const size_t eb = elem_bytes(c);
+  const size_t halves = c->expert_act == MOE_ACT_GELU ? 1 : 2;
+  if (ad && (ad->a_gate_up || ad->a_down)) {
+    k.plan = take(adapter_plan_bytes(adapter_shape(c, ad->n_adapters, ad->rank, false)));
+    if (ad->a_gate_up) {
+      k.pre = take(eb * halves * (size_t)(c->T * c->top_k) * c->d_ff);
+      if (c->weight_format == MOE_W_E4M3) k.x_perm = take(eb * (size_t)(c->T * c->top_k) * c->d_model);
+    }
+  }
+  if (ad && (ad->a_gate_up_shared || ad->a_down_shared)) {
+    k.plan_s = take(adapter_plan_bytes(adapter_shape(c, ad->n_adapters, ad->rank, true)));
+    if (ad->a_gate_up_shared) k.pre_s = take(eb * halves * (size_t)c->T * c->d_ff_shared);
+  }
+  k.total = off;
+  return k;
+}
+
+moe_status check_adapters(const moe_config* c, const moe_adapters* ad) {
+  if (ad == nullptr) return MOE_OK;
+  const bool shared = ad->a_gate_up_shared || ad->b_gate_up_shared || ad->a_down_shared || ad->b_down_shared;
+  const moe_adapter_config ac{ad->n_adapters, ad->rank, shared ? 1 : 0, 0};
+  const moe_status st = check_adapter_config(c, &ac);
+  if (st != MOE_OK) return st;
+  const void* p[] = {ad->token_adapter, ad->scale,         ad->a_gate_up,        ad->b_gate_up,     ad->a_down,
+                     ad->b_down,        ad->a_gate_up_shared, ad->b_gate_up_shared, ad->a_down_shared, ad->b_down_shared};
+  for (const void* q : p)
+    if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
+  for (int i = 2; i < 10; i += 2)
+    if ((p[i] == nullptr) != (p[i + 1] == nullptr)) return MOE_ERR_INVALID_ARG;  // a without its b
+  if (c->T > 0 && (!ad->token_adapter || !ad->scale)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// One group of experts (routed or shared) with adapters: the plan, the first
+// product (without its activation where it has adapters, which then add and
+// activate), the second product, its adapters.  a_quantized as in run_ffn.
+cudaError_t run_adapted_ffn(const moe_config* c, const Carve& k, const moe_adapters* ad, void* plan, void* pre,
+                            const void* x, const int32_t* offsets, const int32_t* perm, int G, int64_t rows, int f,
+                            const void* w_gu, const void* w_d, void* h, void* y, bool shared, bool a_quantized,
+                            cudaStream_t s) {
+  const AdapterShape sh = adapter_shape(c, ad->n_adapters, ad->rank, shared);
+  const void* a1 = shared ? ad->a_gate_up_shared : ad->a_gate_up;
+  const void* b1 = shared ? ad->b_gate_up_shared : ad->b_gate_up;
+  const void* a2 = shared ? ad->a_down_shared : ad->a_down;
+  const void* b2 = shared ? ad->b_down_shared : ad->b_down;
+  cudaError_t e = launch_adapter_plan(sh, offsets, perm, ad->token_adapter, plan, k.status, true, s);
+  if (e != cudaSuccess) return e;
+  e = run_ffn(c, k, x, offsets, G, rows, f, w_gu, w_d, a1 ? pre : h, y, s, shared, a_quantized, true,
+              a1 ? kFfnGemm1Plain : kFfnGemm1);
+  if (e != cudaSuccess) return e;
+  if (a1) {
+    e = launch_adapter_apply(sh, AdapterApply{true, x, a1, b1, ad->scale, pre, h, plan}, true, s);
+    if (e != cudaSuccess) return e;
+  }
+  e = run_ffn(c, k, x, offsets, G, rows, f, w_gu, w_d, h, y, s, shared, true, true, kFfnGemm2);
+  if (e != cudaSuccess || !a2) return e;
+  return launch_adapter_apply(sh, AdapterApply{false, h, a2, b2, ad->scale, y, y, plan}, true, s);
 }
 
 }  // namespace
@@ -277,6 +391,7 @@ const char* moe_status_string(moe_status s) {
     case MOE_ERR_CUDA: return "CUDA error";
     case MOE_ERR_TIMEOUT: return "device wait timed out";
     case MOE_ERR_BAD_EXPERT_ID: return "expert id out of range";
+    case MOE_ERR_BAD_ADAPTER_ID: return "adapter id out of range";
   }
   return "unknown status";
 }
@@ -505,6 +620,119 @@ moe_status moe_forward_traced(const moe_config* cfg, const void* x, const void* 
   return MOE_OK;
 }
 
+size_t moe_adapter_plan_bytes(const moe_config* cfg, const moe_adapter_config* ad) {
+  if (check_adapter_config(cfg, ad) != MOE_OK) return 0;
+  return adapter_plan_bytes(adapter_shape(cfg, ad->n_adapters, ad->rank, ad->shared != 0));
+}
+
+moe_status moe_adapter_plan(const moe_config* cfg, const moe_adapter_config* ad, const int32_t* offsets,
+                            const int32_t* perm, const int32_t* token_adapter, void* plan, size_t plan_bytes,
+                            moe_stream_t stream) {
+  moe_status st = check_adapter_config(cfg, ad);
+  if (st != MOE_OK) return st;
+  const AdapterShape s = adapter_shape(cfg, ad->n_adapters, ad->rank, ad->shared != 0);
+  if (!plan || !aligned256(plan)) return MOE_ERR_INVALID_ARG;
+  if (plan_bytes < adapter_plan_bytes(s)) return MOE_ERR_WORKSPACE;
+  if (cfg->T > 0 && (!token_adapter || !aligned16(token_adapter) || !aligned16(offsets) || !aligned16(perm) ||
+                     (ad->shared ? offsets || perm : !offsets || !perm)))
+    return MOE_ERR_INVALID_ARG;
+  DeviceGuard g;
+  if ((st = enter(g, plan, stream)) != MOE_OK) return st;
+  MOE_CUDA_TRY(cudaMemsetAsync(plan, 0, kAdapterHeader, stream));
+  MOE_CUDA_TRY(launch_adapter_plan(s, offsets, perm, token_adapter, plan, static_cast<int*>(plan), false, stream));
+  return MOE_OK;
+}
+
+moe_status moe_adapter_gate_up(const moe_config* cfg, const moe_adapter_config* ad, void* plan, size_t plan_bytes,
+                               const void* x, const void* a, const void* b, const float* scale, const void* pre,
+                               void* h, moe_stream_t stream) {
+  return adapter_apply(cfg, ad, true, plan, plan_bytes, x, a, b, scale, pre, h, stream);
+}
+
+moe_status moe_adapter_down(const moe_config* cfg, const moe_adapter_config* ad, void* plan, size_t plan_bytes,
+                            const void* h, const void* a, const void* b, const float* scale, const void* base,
+                            void* y, moe_stream_t stream) {
+  return adapter_apply(cfg, ad, false, plan, plan_bytes, h, a, b, scale, base, y, stream);
+}
+
+size_t moe_forward_routed_workspace_bytes(const moe_config* cfg, const moe_adapters* adapters) {
+  if (check_config(cfg) != MOE_OK || check_adapters(cfg, adapters) != MOE_OK) return 0;
+  return carve_routed(cfg, adapters, nullptr).total;
+}
+
+moe_status moe_forward_routed(const moe_config* cfg, const moe_route_config* route, const moe_adapters* adapters,
+                              const void* x, const void* logits, const float* select_bias, const void* w_gate_up,
+                              const void* w_down, const void* ws_gate_up, const void* ws_down, void* y,
+                              int32_t* opt_topk_ids, float* opt_topk_w, int32_t* opt_counts, void* ws,
+                              size_t ws_bytes, moe_stream_t stream) {
+  moe_status st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if ((st = check_route_config(route)) != MOE_OK) return st;
+  if (route->T != cfg->T || route->n_experts != cfg->n_experts || route->top_k != cfg->top_k)
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_adapters(cfg, adapters)) != MOE_OK) return st;
+  if (ws == nullptr || !aligned256(ws)) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < carve_routed(cfg, adapters, nullptr).total) return MOE_ERR_WORKSPACE;
+  if (opt_counts && !aligned16(opt_counts)) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) {  // nothing to read or write: clear the status word and the optional counts
+    DeviceGuard g;
+    if ((st = enter(g, ws, stream)) != MOE_OK) return st;
+    MOE_CUDA_TRY(cudaMemsetAsync(ws, 0, 16, stream));
+    if (opt_counts) MOE_CUDA_TRY(cudaMemsetAsync(opt_counts, 0, sizeof(int32_t) * cfg->n_experts, stream));
+    return MOE_OK;
+  }
+  if (!x || !logits || !w_gate_up || !w_down || !y || !aligned16(x) || !aligned16(logits) || !aligned16(w_gate_up) ||
+      !aligned16(w_down) || !aligned16(y) || !aligned16(select_bias) || !aligned16(opt_topk_ids) ||
+      !aligned16(opt_topk_w))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->n_shared > 0 && (!ws_gate_up || !ws_down || !aligned16(ws_gate_up) || !aligned16(ws_down)))
+    return MOE_ERR_INVALID_ARG;
+  DeviceGuard g;
+  if ((st = enter(g, ws, stream)) != MOE_OK) return st;
+  if ((st = g.same_device(x)) != MOE_OK) return st;
+  if ((st = g.same_device(logits)) != MOE_OK) return st;
+  const Carve k = carve(cfg, ws);
+  const RoutedCarve rk = carve_routed(cfg, adapters, ws);
+  // everything that has to be zero is cleared ahead of the chain of launches (pdl.cuh)
+  MOE_CUDA_TRY(cudaMemsetAsync(k.status, 0, 16, stream));
+  if (k.counters) MOE_CUDA_TRY(cudaMemsetAsync(k.counters, 0, sizeof(int) * (size_t)k.counter_cap, stream));
+  if (rk.plan) MOE_CUDA_TRY(cudaMemsetAsync(rk.plan, 0, kAdapterHeader, stream));
+  if (rk.plan_s) MOE_CUDA_TRY(cudaMemsetAsync(rk.plan_s, 0, kAdapterHeader, stream));
+  int32_t* ids = opt_topk_ids ? opt_topk_ids : k.ids;
+  float* w = opt_topk_w ? opt_topk_w : k.w;
+  int32_t* counts = opt_counts ? opt_counts : k.counts;
+  MOE_CUDA_TRY(launch_route_topk(route_args(route, logits, select_bias, ids, w), stream));
+  // 8-bit experts: the dispatch writes codes straight from x (moe_forward),
+  // unless adapters need the rows themselves
+  const bool e4m3 = cfg->weight_format == MOE_W_E4M3;
+  void* x_perm = e4m3 ? rk.x_perm : k.x_perm;
+  PermuteArgs pa{ids, x, counts, k.offsets, k.perm, k.row_of, x_perm, k.chunk_counts, cfg->T * cfg->top_k,
+                 cfg->top_k, cfg->d_model, cfg->n_experts, (int)elem_bytes(cfg), k.status, capacity_rows(cfg), true,
+                 -1};
+  MOE_CUDA_TRY(launch_permute(pa, stream));
+  const bool codes = e4m3 && x_perm == nullptr;
+  if (codes)
+    MOE_CUDA_TRY(
+        launch_gather_quantize_e4m3(x, k.row_of, cfg->top_k, cfg->T, cfg->d_model, k.xq, k.sx, true, stream));
+  const int64_t rows = cfg->T * cfg->top_k;
+  if (rk.plan)
+    MOE_CUDA_TRY(run_adapted_ffn(cfg, k, adapters, rk.plan, rk.pre, x_perm, k.offsets, k.perm, cfg->n_experts, rows,
+                                 cfg->d_ff, w_gate_up, w_down, k.h, k.y_perm, false, codes, stream));
+  else
+    MOE_CUDA_TRY(run_ffn(cfg, k, x_perm, k.offsets, cfg->n_experts, rows, cfg->d_ff, w_gate_up, w_down, k.h,
+                         k.y_perm, stream, false, codes, true));
+  if (rk.plan_s)
+    MOE_CUDA_TRY(run_adapted_ffn(cfg, k, adapters, rk.plan_s, rk.pre_s, x, nullptr, nullptr, 1, cfg->T,
+                                 cfg->d_ff_shared, ws_gate_up, ws_down, k.h_s, k.y_s, true, false, stream));
+  else if (cfg->n_shared > 0)
+    MOE_CUDA_TRY(run_ffn(cfg, k, x, nullptr, 1, cfg->T, cfg->d_ff_shared, ws_gate_up, ws_down, k.h_s, k.y_s, stream,
+                         true, false, true));
+  CombineArgs ca{k.y_perm, k.row_of, w, cfg->n_shared > 0 ? k.y_s : nullptr, y, cfg->T, cfg->top_k,
+                 cfg->d_model, cfg->dtype == MOE_BF16, true};
+  MOE_CUDA_TRY(launch_combine(ca, stream));
+  return MOE_OK;
+}
+
 moe_status moe_device_status(const void* ws, size_t ws_bytes, moe_stream_t stream) {
   if (ws == nullptr || ws_bytes < 16 || (reinterpret_cast<uintptr_t>(ws) % kAlign) != 0) return MOE_ERR_INVALID_ARG;
   MOE_CUDA_TRY(cudaStreamSynchronize(stream));
@@ -512,6 +740,7 @@ moe_status moe_device_status(const void* ws, size_t ws_bytes, moe_stream_t strea
   MOE_CUDA_TRY(cudaMemcpy(&v, ws, sizeof(int), cudaMemcpyDeviceToHost));
   if (v == kDevTimeout) return MOE_ERR_TIMEOUT;
   if (v == kDevBadExpertId) return MOE_ERR_BAD_EXPERT_ID;
+  if (v == kDevBadAdapterId) return MOE_ERR_BAD_ADAPTER_ID;
   return v == 0 ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -36,7 +36,7 @@ constexpr int kChunk = kWarps * kPerWarp;     // assignments per block
 
 __global__ void __launch_bounds__(kThreads) permute_count_kernel(const int32_t* __restrict__ ids, int64_t n,
                                                                  int E, int32_t* chunk_counts, int n_chunks,
-                                                                 int* status) {
+                                                                 int* status, int min_id) {
   extern __shared__ int hist[];
   for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
   __syncthreads();
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads) permute_count_kernel(const int32_t* 
   for (int64_t i = base + threadIdx.x; i < end; i += kThreads) {
     const int e = ids[i];
     if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
-    else set_status(status, kDevBadExpertId);
+    else if (e < min_id || e >= E) set_status(status, kDevBadExpertId);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kThreads) chunk_counts[(int64_t)blockIdx.x * E + e] = hist[e];
@@ -178,7 +178,7 @@ constexpr int kSmallThreads = 1024;  // >= kMaxExperts: one expert per thread in
 
 __global__ void __launch_bounds__(kSmallThreads)
     permute_small_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t capacity, int32_t* counts,
-                         int32_t* offsets, int32_t* perm, int32_t* row_of, int* status) {
+                         int32_t* offsets, int32_t* perm, int32_t* row_of, int* status, int min_id) {
   extern __shared__ int sm[];  // hist[E], base[E], run[E]
   __shared__ int warp_sums[kSmallThreads / 32];
   int* hist = sm;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   for (int64_t i = tid; i < n; i += kSmallThreads) {
     const int e = ids[i];
     if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
-    else set_status(status, kDevBadExpertId);
+    else if (e < min_id || e >= E) set_status(status, kDevBadExpertId);
   }
   __syncthreads();
   // exclusive scan of the rows each expert keeps
@@ -266,7 +266,7 @@ constexpr int kMidWarps = kSmallThreads / 32;
 
 __global__ void __launch_bounds__(kSmallThreads)
     permute_mid_kernel(const int32_t* __restrict__ ids, int64_t n, int E, int64_t capacity, int32_t* counts,
-                       int32_t* offsets, int32_t* perm, int32_t* row_of, int* status) {
+                       int32_t* offsets, int32_t* perm, int32_t* row_of, int* status, int min_id) {
   __shared__ int wrank[kMidWarps][kMidExperts];  // per warp and expert: its count, then its first rank
   __shared__ int base[kMidExperts];
   __shared__ int warp_sums[kMidWarps];
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     if (i < hi) {
       e = ids[i];
       if (e < 0 || e >= E) {
-        set_status(status, kDevBadExpertId);
+        if (e < min_id || e >= E) set_status(status, kDevBadExpertId);
         e = -1;
       }
     }
@@ -399,16 +399,16 @@ cudaError_t launch_permute(const PermuteArgs& a, cudaStream_t stream) {
   if (a.n_assign <= kSmallDispatch) {
     const cudaError_t e = launch_maybe_chained(permute_small_kernel, dim3(1), dim3(kSmallThreads),
                                                3 * sizeof(int) * a.E, stream, a.chained, a.ids, a.n_assign, a.E,
-                                               a.capacity, a.counts, a.offsets, a.perm, a.row_of, a.status);
+                                               a.capacity, a.counts, a.offsets, a.perm, a.row_of, a.status, a.min_id);
     if (e != cudaSuccess) return e;
   } else if (a.n_assign <= kMidDispatch && a.E <= kMidExperts) {
     const cudaError_t e = launch_maybe_chained(permute_mid_kernel, dim3(1), dim3(kSmallThreads), 0, stream,
                                                a.chained, a.ids, a.n_assign, a.E, a.capacity, a.counts, a.offsets,
-                                               a.perm, a.row_of, a.status);
+                                               a.perm, a.row_of, a.status, a.min_id);
     if (e != cudaSuccess) return e;
   } else {
     permute_count_kernel<<<n_chunks, kThreads, sizeof(int) * a.E, stream>>>(a.ids, a.n_assign, a.E,
-                                                                            a.chunk_counts, n_chunks, a.status);
+                                                                            a.chunk_counts, n_chunks, a.status, a.min_id);
     permute_scan_kernel<<<1, kScanThreads, 0, stream>>>(a.chunk_counts, n_chunks, a.E, a.counts, a.offsets,
                                                         a.capacity);
     permute_scatter_kernel<<<n_chunks, kThreads, sizeof(int) * kWarps * a.E, stream>>>(

@@ -33,6 +33,7 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "pdl.cuh"
 
 namespace moe {
 namespace {
@@ -256,6 +257,7 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
   const T* __restrict__ logits = static_cast<const T*>(p.logits);
   const int64_t step = (int64_t)gridDim.x * kWarps;
   int64_t t = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
+  if (threadIdx.x == 0) grid_launch_dependents();  // the dispatch may be scheduled (it waits for these ids)
   if (t >= p.T) return;
 
   float next[NC];
