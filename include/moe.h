@@ -424,7 +424,7 @@ moe_status moe_combine_backward(const moe_config* cfg, const void* grad_y, const
    d_ff_shared for d_ff).  Products accumulate in fp32; the adapter's term is
    added to the base in fp32 and rounded once. */
 typedef struct {
-  int32_t n_adapters;       /* N, 1..65536                                     */
+  int32_t n_adapters;       /* N, 1..65536; E * N below 2^23 - 2                */
   int32_t rank;             /* r, a multiple of 8, 8..128; an adapter of a
                                lower rank is filled up with zeros              */
   int32_t shared;           /* 0: the routed experts, 1: the shared expert     */

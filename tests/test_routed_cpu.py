@@ -132,6 +132,9 @@ def test_adapter_argument_refusals(L):
     assert need > 0 and need % 256 == 0
     assert _plan(L, cfg, None) == INVALID and _apply(L, cfg, None) == INVALID
     assert _plan(L, _cfg(top_k=9), ad) == INVALID
+    many = _cfg(n_experts=1024)
+    assert _plan(L, many, moe.make_adapter_config(8192, 8)) == UNSUPPORTED  # experts x adapters
+    assert moe.moe_adapter_plan_bytes(many, moe.make_adapter_config(8191, 8)) > 0
     for name in ("offsets", "perm", "ta", "plan"):
         assert _plan(L, cfg, ad, **{name: None}) == INVALID
         assert _plan(L, cfg, ad, **{name: 264}) == INVALID

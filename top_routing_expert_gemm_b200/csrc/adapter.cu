@@ -34,7 +34,8 @@ constexpr int kChunkRows = 256;  // rows a plan block sorts
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kSkip = 0x7fffffff;  // key of a row that is not there
+static_assert((int64_t)(kAdapterMaxPairs + 1) * kChunkRows < (int64_t(1) << 31), "keys of the plan are 31 bits");
+constexpr int kSkip = 0x7fffff;  // pair of a row that is not there (kMaxPairs - 1 is below)
 
 struct Tile {
   int start;    // first position in `order`
@@ -56,7 +57,12 @@ struct PlanParams {
   int* status;
 };
 
-__global__ void __launch_bounds__(kChunkRows) adapter_plan_kernel(const PlanParams p) {
+// Four threads per row: each compares the row's key with a quarter of the
+// chunk's.  A key holds (expert, adapter) above the row's place in the chunk, so
+// all keys differ and one comparison ranks stably.
+constexpr int kPlanThreads = 4 * kChunkRows;
+
+__global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanParams p) {
   extern __shared__ int s_off[];  // [E+1]
   __shared__ __align__(16) int keys[kChunkRows];
   __shared__ int sorted[kChunkRows];
@@ -65,62 +71,81 @@ __global__ void __launch_bounds__(kChunkRows) adapter_plan_kernel(const PlanPara
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   grid_dependency_wait();  // the dispatch (programmatic launch)
   if (tid == 0) grid_launch_dependents();
-  if (p.offsets)
-    for (int e = tid; e <= p.E; e += kChunkRows) s_off[e] = p.offsets[e];
-  __syncthreads();
   const int64_t row0 = (int64_t)blockIdx.x * kChunkRows;
-  const int64_t live = p.offsets ? min((int64_t)s_off[p.E], p.rows) : p.rows;
   const int64_t row = row0 + tid;
-  int key = kSkip;
-  if (row < live) {
-    const int64_t token = p.perm ? p.perm[row] / p.k : row;
-    int a = p.token_adapter[token];
-    if (a >= p.N) {
-      set_status(p.status, kDevBadAdapterId);
-      a = -1;
-    }
-    int e = 0;
-    if (p.offsets) {  // the last expert whose rows start at or before this one
-      int lo = 0, hi = p.E;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_off[mid] <= row) lo = mid;
-        else hi = mid;
-      }
-      e = lo;
-    }
-    key = a < 0 ? -1 : e * p.N + a;  // rows without an adapter form one run, whatever their expert
-  }
-  keys[tid] = key;
+  const bool mine_to_load = tid < kChunkRows && row < p.rows;
+  const int slot = mine_to_load && p.perm ? p.perm[row] : 0;  // garbage behind the last row: not used there
+  if (p.offsets)
+    for (int e = tid; e <= p.E; e += kPlanThreads) s_off[e] = p.offsets[e];
   __syncthreads();
-  // stable rank: rows with a smaller key, or the same key and earlier
-  int rank = 0;
-  const int4* k4 = reinterpret_cast<const int4*>(keys);
-#pragma unroll 8
-  for (int i = 0; i < kChunkRows / 4; ++i) {
-    const int4 q = k4[i];
-    rank += (q.x < key || (q.x == key && 4 * i < tid)) + (q.y < key || (q.y == key && 4 * i + 1 < tid)) +
-            (q.z < key || (q.z == key && 4 * i + 2 < tid)) + (q.w < key || (q.w == key && 4 * i + 3 < tid));
+  const int64_t live = p.offsets ? min((int64_t)s_off[p.E], p.rows) : p.rows;
+  if (tid < kChunkRows) {
+    int pair = kSkip;
+    if (row < live) {
+      int a = p.token_adapter[p.perm ? slot / p.k : row];
+      if (a >= p.N) {
+        set_status(p.status, kDevBadAdapterId);
+        a = -1;
+      }
+      int e = 0;
+      if (a >= 0 && p.offsets) {  // the last expert whose rows start at or before this one
+        int lo = 0, hi = p.E;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_off[mid] <= row) lo = mid;
+          else hi = mid;
+        }
+        e = lo;
+      }
+      pair = a < 0 ? 0 : e * p.N + a + 1;  // rows without an adapter form one run, whatever their expert
+    }
+    keys[tid] = pair * kChunkRows + tid;
   }
-  sorted[rank] = key;
-  if (key != kSkip) p.order[row0 + rank] = (int32_t)row;
+  __syncthreads();
+  {
+    const int i = tid / 4, quarter = tid % 4;
+    const int key = keys[i];
+    int rank = 0;
+    const int4* k4 = reinterpret_cast<const int4*>(keys);
+#pragma unroll
+    for (int j = 0; j < kChunkRows / 16; ++j) {
+      const int4 q = k4[4 * j + quarter];
+      rank += (q.x < key) + (q.y < key) + (q.z < key) + (q.w < key);
+    }
+    rank += __shfl_xor_sync(kFull, rank, 1);
+    rank += __shfl_xor_sync(kFull, rank, 2);
+    if (quarter == 0) {
+      sorted[rank] = key / kChunkRows;
+      if (key / kChunkRows != kSkip) p.order[row0 + rank] = (int32_t)(row0 + i);
+    }
+  }
   __syncthreads();
   // position tid of the sorted chunk starts a tile where its run starts, and
   // every TM rows from there
-  const int mine = sorted[tid];
-  int first = 0;
+  const int mine = tid < kChunkRows ? sorted[tid] : kSkip;
+  bool head = false;
+  int end = 0;
   if (mine != kSkip) {
-    int lo = 0, hi = tid;  // first position of the run (keys ascend)
+    int lo = 0, hi = tid;  // first position of the run (the pairs ascend)
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (sorted[mid] < mine) lo = mid + 1;
       else hi = mid;
     }
-    first = lo;
+    head = (tid - lo) % p.TM == 0;
+    if (head) {
+      lo = tid + 1;
+      hi = min(kChunkRows, tid + p.TM);
+      while (lo < hi) {  // first position behind the tile
+        const int mid = (lo + hi) >> 1;
+        if (sorted[mid] == mine) lo = mid + 1;
+        else hi = mid;
+      }
+      end = lo;
+    }
   }
-  const bool head = mine != kSkip && (tid - first) % p.TM == 0;
   const unsigned heads = __ballot_sync(kFull, head);
-  if (lane == 0) warp_sums[warp] = __popc(heads);
+  if (lane == 0 && tid < kChunkRows) warp_sums[warp] = __popc(heads);
   __syncthreads();
   if (tid == 0) {
     int n = 0;
@@ -133,10 +158,9 @@ __global__ void __launch_bounds__(kChunkRows) adapter_plan_kernel(const PlanPara
   }
   __syncthreads();
   if (head) {
-    int n = 1;
-    while (n < p.TM && tid + n < kChunkRows && sorted[tid + n] == mine) ++n;
     const int at = s_base + warp_sums[warp] + __popc(heads & ((1u << lane) - 1u));
-    p.tiles[at] = Tile{(int)(row0 + tid), n, mine < 0 ? -1 : mine % p.N, mine < 0 ? 0 : mine / p.N};
+    const int pair = mine - 1;
+    p.tiles[at] = Tile{(int)(row0 + tid), end - tid, pair < 0 ? -1 : pair % p.N, pair < 0 ? 0 : pair / p.N};
   }
 }
 
@@ -162,13 +186,43 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 
 __device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(static_cast<const uint4*>(p)); }
 
+// Asynchronous copies into the warp's own ring in shared memory: a lane reads
+// back only what it copied itself, so a wait_group is all the synchronisation
+// there is.  Without `on` the destination is zeroed and nothing is read.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Stages of a warp's ring whose stage takes `bytes`: what two blocks per SM
+// leave each of their warps (13.5 KiB), one stage at least, four at most
+constexpr int ring_stages(int bytes) { return bytes * 4 <= 13824 ? 4 : bytes * 3 <= 13824 ? 3 : bytes * 2 <= 13824 ? 2 : 1; }
+
 // MT row tiles of 16, up to RT rank tiles of 8.  A lane takes 8 consecutive
 // inputs of a row with one 16-byte load and uses them as the k indices 2t,
 // 2t+1, 2t+8, 2t+9 of two instructions: the sum runs over all inputs, so any
 // assignment of inputs to k serves as long as x and A agree.
+constexpr int kUnit = 64;  // inputs per warp and round: whole 128-byte lines of every row
 template <int MT, int RT>
-__global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkParams p) {
-  __shared__ __align__(16) float red[kWarps / 2][MT * 16 * RT * 8];
+constexpr int shrink_stage() { return 2 * (2 * MT + RT) * 512; }
+template <int MT, int RT>
+constexpr int shrink_smem() {
+  const int ring = kWarps * ring_stages(shrink_stage<MT, RT>()) * shrink_stage<MT, RT>();
+  const int red = kWarps / 2 * MT * 16 * RT * 8 * 4;  // the fold of the warps' sums, over the drained rings
+  return ring > red ? ring : red;
+}
+template <int MT, int RT>
+__global__ void __launch_bounds__(kThreads, MT * RT <= 8 ? 2 : 1) adapter_shrink_kernel(const ShrinkParams p) {
+  constexpr int kStage = shrink_stage<MT, RT>(), kStages = ring_stages(kStage);
+  extern __shared__ __align__(16) uint8_t smem[];
+  float(*red)[MT * 16 * RT * 8] = reinterpret_cast<float(*)[MT * 16 * RT * 8]>(smem);
+  uint8_t* ring_ptr = smem + threadIdx.x / 32 * (kStages * kStage) + threadIdx.x % 32 * 16;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_ptr);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int g = lane / 4, t4 = lane % 4;
   grid_dependency_wait();
@@ -197,31 +251,55 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkPa
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
 
-    constexpr int kUnit = 64;  // inputs per warp and round: whole 128-byte lines of every row
-    for (int k0 = k_lo + warp * kUnit; k0 < k_hi; k0 += kWarps * kUnit) {
-      uint4 xv[2][MT][2], av[2][RT];
+    auto issue = [&](int k0, int slot) {
+      const uint32_t dst = ring + slot * kStage;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int k = k0 + 32 * c + 8 * t4;
         const bool in = k < k_hi;  // K and k_block are multiples of 8
 #pragma unroll
-        for (int n = 0; n < RT; ++n)
-          av[c][n] = in && n * 8 + g < p.r ? ldg16(a + (int64_t)(n * 8 + g) * p.K + k) : make_uint4(0, 0, 0, 0);
+        for (int n = 0; n < RT; ++n) {
+          const bool on = in && n * 8 + g < p.r;
+          copy16(dst + (c * RT + n) * 512, on ? a + (int64_t)(n * 8 + g) * p.K + k : a, on);
+        }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            xv[c][m][h] = in && row[m][h] >= 0 ? ldg16(x + row[m][h] * p.K + k) : make_uint4(0, 0, 0, 0);
+          for (int h = 0; h < 2; ++h) {
+            const bool on = in && row[m][h] >= 0;
+            copy16(dst + (2 * RT + (c * MT + m) * 2 + h) * 512, on ? x + row[m][h] * p.K + k : x, on);
+          }
       }
+    };
+    const int k_first = k_lo + warp * kUnit;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+    for (int d = 0; d < kStages - 1; ++d) {
+      if (k_first + d * kWarps * kUnit < k_hi) issue(k_first + d * kWarps * kUnit, d);
+      copies_commit();
+    }
+    int slot = 0;
+    for (int k0 = k_first; k0 < k_hi; k0 += kWarps * kUnit) {
+      const int ahead = k0 + (kStages - 1) * kWarps * kUnit;
+      if (ahead < k_hi) issue(ahead, slot == 0 ? kStages - 1 : slot - 1);
+      copies_commit();
+      copies_wait<kStages - 1>();
+      const uint4* st = reinterpret_cast<const uint4*>(ring_ptr + slot * kStage);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+      for (int c = 0; c < 2; ++c) {
+        uint4 av[RT];
+#pragma unroll
+        for (int n = 0; n < RT; ++n) av[n] = st[(c * RT + n) * 32];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint4 x0 = st[(2 * RT + (c * MT + m) * 2) * 32], x1 = st[(2 * RT + (c * MT + m) * 2 + 1) * 32];
 #pragma unroll
           for (int n = 0; n < RT; ++n) {
-            mma_bf16(acc[m][n], xv[c][m][0].x, xv[c][m][1].x, xv[c][m][0].y, xv[c][m][1].y, av[c][n].x, av[c][n].y);
-            mma_bf16(acc[m][n], xv[c][m][0].z, xv[c][m][1].z, xv[c][m][0].w, xv[c][m][1].w, av[c][n].z, av[c][n].w);
+            mma_bf16(acc[m][n], x0.x, x1.x, x0.y, x1.y, av[n].x, av[n].y);
+            mma_bf16(acc[m][n], x0.z, x1.z, x0.w, x1.w, av[n].z, av[n].w);
           }
+        }
+      }
+      if (++slot == kStages) slot = 0;
     }
     // the warps' sums: halves are folded, in a fixed order
 #pragma unroll
@@ -262,6 +340,7 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_kernel(const ShrinkPa
               *reinterpret_cast<float2*>(u + (int64_t)i * p.r + c) = make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
           }
     }
+    __syncthreads();  // the fold is read before the next tile's copies land there
   }
 }
 
@@ -335,7 +414,7 @@ struct ExpandParams {
   int64_t rows;
   int r, E, S;
   int n_out, n_res;  // columns of base and of the result
-  int col_block;     // result columns per block (blockIdx.x), a multiple of 32 * kWarps
+  int col_block;     // result columns per block (blockIdx.x), whole rounds of the block's warps
   bool in_place;     // base is the result and nothing is applied to it: rows without an adapter are right
 };
 
@@ -344,17 +423,40 @@ __device__ __forceinline__ float finish(float v, float up) {
   return EPI == kEpiSwiGLU ? silu_f(v) * up : EPI == kEpiGELU ? gelu_f(v) : v;
 }
 
-// A warp takes 32 result columns (and, for SwiGLU, the matching 32 up
-// columns) of the tile's MT * 16 rows.  Column 2t+i of instruction j stands for
-// result column 8t + 2j + i, so a lane ends with 8 consecutive columns of a
-// row: base comes and the result leaves in 16-byte vectors.  U enters as a sum
-// of two bf16 values (16 bits of mantissa), so its rounding does not show
-// beside the result's own.
-template <int MT, int RK, int EPI>
-__global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const ExpandParams p) {
+// SiLU for results that are rounded to bf16: __expf and __fdividef are off by
+// under 2^-19 of the value for any argument that leaves one above 2^-126,
+// against half a bf16 step of 2^-9; expf and the IEEE division made the kernel
+// issue bound (285 against 94 us for the 2048-token batch below).
+__device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
+template <int EPI>
+__device__ __forceinline__ float finish_bf16(float v, float up) {
+  return EPI == kEpiSwiGLU ? silu_fast(v) * up : EPI == kEpiGELU ? gelu_f(v) : v;
+}
+
+// A warp takes 16 rows of the tile and 32 result columns (and, for SwiGLU, the
+// matching 32 up columns) per round; the block's warps cover the tile's WR row
+// groups side by side, so they share B through L1.  Column 2t+i of instruction
+// j stands for result column 8t + 2j + i, so a lane ends with 8 consecutive
+// columns of a row: base comes and the result leaves in 16-byte vectors.  U
+// enters as a sum of two bf16 values (16 bits of mantissa), so its rounding
+// does not show beside the result's own.
+template <int RK, int EPI>
+constexpr int expand_stage() { return (EPI == kEpiSwiGLU ? 2 : 1) * (2 * 512 + 4 * RK * 256); }
+template <int RK, int EPI>
+constexpr int expand_smem() { return kWarps * ring_stages(expand_stage<RK, EPI>()) * expand_stage<RK, EPI>(); }
+template <int WR, int RK, int EPI>
+__global__ void __launch_bounds__(kThreads, RK <= 2 ? 2 : 1) adapter_expand_kernel(const ExpandParams p) {
   constexpr int H = EPI == kEpiSwiGLU ? 2 : 1;
+  constexpr int kStage = expand_stage<RK, EPI>(), kStages = ring_stages(kStage);
+  constexpr int kB = 2 * H * 512;  // base first, then B
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint8_t* ring_ptr = smem + threadIdx.x / 32 * (kStages * kStage);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_ptr);
+  constexpr int CG = kWarps / WR;  // column groups of a round
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int g = lane / 4, t4 = lane % 4;
+  const int i0 = warp % WR * 16;
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   const int n_tiles = *p.n_tiles;
@@ -363,55 +465,24 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const ExpandPa
   for (int t = blockIdx.y; t < n_tiles; t += gridDim.y) {
     const Tile tile = p.tiles[t];
     const bool has = tile.adapter >= 0;
-    if (!has && p.in_place) continue;
-    int64_t row[MT][2];
-    uint32_t hi[MT][RK][4], lo[MT][RK][4];  // U fragments: rows g, g+8; ranks 16 c + 4 t4 + {0,1} and {2,3}
+    if ((!has && p.in_place) || i0 >= tile.count) continue;
+    int64_t row[2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = m * 16 + h * 8 + g;
-        row[m][h] = i < tile.count ? p.order[tile.start + i] : -1;
-#pragma unroll
-        for (int c = 0; c < RK; ++c) {
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          const int k = 16 * c + 4 * t4;
-          if (has && i < tile.count && k < p.r) {
-            const float* u = p.u + (int64_t)(tile.start + i) * p.r + k;
-            for (int s = 0; s < p.S; ++s) {
-              const float4 w = __ldg(reinterpret_cast<const float4*>(u + (int64_t)s * p.rows * p.r));
-              v.x += w.x;
-              v.y += w.y;
-              v.z += w.z;
-              v.w += w.w;
-            }
-            const float sc = p.scale[tile.adapter];
-            v = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
-          }
-          hi[m][c][h] = pack_bf16x2(v.x, v.y);
-          hi[m][c][2 + h] = pack_bf16x2(v.z, v.w);
-          const __nv_bfloat162 p0 = *reinterpret_cast<__nv_bfloat162*>(&hi[m][c][h]);
-          const __nv_bfloat162 p1 = *reinterpret_cast<__nv_bfloat162*>(&hi[m][c][2 + h]);
-          lo[m][c][h] = pack_bf16x2(v.x - __low2float(p0), v.y - __high2float(p0));
-          lo[m][c][2 + h] = pack_bf16x2(v.z - __low2float(p1), v.w - __high2float(p1));
-        }
-      }
+    for (int h = 0; h < 2; ++h) row[h] = i0 + h * 8 + g < tile.count ? p.order[tile.start + i0 + h * 8 + g] : -1;
     const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(p.b) +
                              ((int64_t)(has ? tile.adapter : 0) * p.E + tile.expert) * p.n_out * p.r;
+    const int c_first = blockIdx.x * p.col_block + warp / WR * 32;
     const int c_end = min(p.n_res, (int)((blockIdx.x + 1) * p.col_block));
-    for (int c0 = blockIdx.x * p.col_block + warp * 32; c0 < c_end; c0 += kWarps * 32) {
+    auto issue = [&](int c0, int slot) {
       const int col = c0 + 8 * t4;  // this lane's 8 result columns
-      const bool in = col < p.n_res;
-      uint4 bs[MT][2][H];
+      const uint32_t dst = ring + slot * kStage;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int q = 0; q < H; ++q)
-            bs[m][h][q] = in && row[m][h] >= 0 ? ldg16(base + row[m][h] * p.n_out + q * p.n_res + col)
-                                               : make_uint4(0, 0, 0, 0);
-      uint2 bv[H][4][RK];
+        for (int q = 0; q < H; ++q) {
+          const bool on = col < p.n_res && row[h] >= 0;
+          copy16(dst + (h * H + q) * 512 + lane * 16, on ? base + row[h] * p.n_out + q * p.n_res + col : base, on);
+        }
 #pragma unroll
       for (int q = 0; q < H; ++q)
 #pragma unroll
@@ -420,43 +491,90 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_kernel(const ExpandPa
 #pragma unroll
           for (int c = 0; c < RK; ++c) {
             const int k = 16 * c + 4 * t4;
-            bv[q][j][c] = has && n < p.n_res && k < p.r
-                              ? __ldg(reinterpret_cast<const uint2*>(b + (int64_t)(q * p.n_res + n) * p.r + k))
-                              : make_uint2(0, 0);
+            const bool on = has && n < p.n_res && k < p.r;
+            copy8(dst + kB + ((q * 4 + j) * RK + c) * 256 + lane * 8,
+                  on ? b + (int64_t)(q * p.n_res + n) * p.r + k : base, on);
+          }
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < kStages - 1; ++d) {
+      if (c_first + d * CG * 32 < c_end) issue(c_first + d * CG * 32, d);
+      copies_commit();
+    }
+    uint32_t hi[RK][4], lo[RK][4];  // U fragments: rows g, g+8; ranks 16 c + 4 t4 + {0,1} and {2,3}
+    const float sc = has ? p.scale[tile.adapter] : 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int c = 0; c < RK; ++c) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int k = 16 * c + 4 * t4;
+        if (has && row[h] >= 0 && k < p.r) {
+          const float* u = p.u + (int64_t)(tile.start + i0 + h * 8 + g) * p.r + k;
+#pragma unroll 4
+          for (int s = 0; s < p.S; ++s) {
+            const float4 w = __ldg(reinterpret_cast<const float4*>(u + (int64_t)s * p.rows * p.r));
+            v.x += w.x;
+            v.y += w.y;
+            v.z += w.z;
+            v.w += w.w;
+          }
+          v = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
+        }
+        hi[c][h] = pack_bf16x2(v.x, v.y);
+        hi[c][2 + h] = pack_bf16x2(v.z, v.w);
+        const __nv_bfloat162 p0 = *reinterpret_cast<__nv_bfloat162*>(&hi[c][h]);
+        const __nv_bfloat162 p1 = *reinterpret_cast<__nv_bfloat162*>(&hi[c][2 + h]);
+        lo[c][h] = pack_bf16x2(v.x - __low2float(p0), v.y - __high2float(p0));
+        lo[c][2 + h] = pack_bf16x2(v.z - __low2float(p1), v.w - __high2float(p1));
+      }
+    }
+    int slot = 0;
+    for (int c0 = c_first; c0 < c_end; c0 += CG * 32) {
+      const int ahead = c0 + (kStages - 1) * CG * 32;
+      if (ahead < c_end) issue(ahead, slot == 0 ? kStages - 1 : slot - 1);
+      copies_commit();
+      copies_wait<kStages - 1>();
+      const int col = c0 + 8 * t4;
+      const bool in = col < p.n_res;
+      const uint8_t* st = ring_ptr + slot * kStage;
+      const uint4* st_base = reinterpret_cast<const uint4*>(st) + lane;
+      const uint2* st_b = reinterpret_cast<const uint2*>(st + kB) + lane;
+      if (++slot == kStages) slot = 0;
+      float acc[H][4][4];
+#pragma unroll
+      for (int q = 0; q < H; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float(&d)[4] = acc[q][j];
+          d[0] = d[1] = d[2] = d[3] = 0.f;
+#pragma unroll
+          for (int c = 0; c < RK; ++c) {
+            const uint2 bv = st_b[((q * 4 + j) * RK + c) * 32];
+            mma_bf16(d, lo[c][0], lo[c][1], lo[c][2], lo[c][3], bv.x, bv.y);
+            mma_bf16(d, hi[c][0], hi[c][1], hi[c][2], hi[c][3], bv.x, bv.y);
           }
         }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float acc[H][4][4];
+      for (int h = 0; h < 2; ++h) {
+        if (!in || row[h] < 0) continue;
+        uint4 bs[H];
 #pragma unroll
-        for (int q = 0; q < H; ++q)
+        for (int q = 0; q < H; ++q) bs[q] = st_base[(h * H + q) * 32];
+        uint32_t o[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float(&d)[4] = acc[q][j];
-            d[0] = d[1] = d[2] = d[3] = 0.f;
+        for (int j = 0; j < 4; ++j) {
+          float v[H][2];
 #pragma unroll
-            for (int c = 0; c < RK; ++c) {
-              mma_bf16(d, lo[m][c][0], lo[m][c][1], lo[m][c][2], lo[m][c][3], bv[q][j][c].x, bv[q][j][c].y);
-              mma_bf16(d, hi[m][c][0], hi[m][c][1], hi[m][c][2], hi[m][c][3], bv[q][j][c].x, bv[q][j][c].y);
-            }
+          for (int q = 0; q < H; ++q) {
+            const uint32_t w = j == 0 ? bs[q].x : j == 1 ? bs[q].y : j == 2 ? bs[q].z : bs[q].w;
+            v[q][0] = __uint_as_float(w << 16) + acc[q][j][2 * h];
+            v[q][1] = __uint_as_float(w & 0xffff0000u) + acc[q][j][2 * h + 1];
           }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!in || row[m][h] < 0) continue;
-          uint32_t o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float v[H][2];
-#pragma unroll
-            for (int q = 0; q < H; ++q) {
-              const uint32_t w = j == 0 ? bs[m][h][q].x : j == 1 ? bs[m][h][q].y : j == 2 ? bs[m][h][q].z : bs[m][h][q].w;
-              v[q][0] = __uint_as_float(w << 16) + acc[q][j][2 * h];
-              v[q][1] = __uint_as_float(w & 0xffff0000u) + acc[q][j][2 * h + 1];
-            }
-            o[j] = pack_bf16x2(finish<EPI>(v[0][0], v[H - 1][0]), finish<EPI>(v[0][1], v[H - 1][1]));
-          }
-          *reinterpret_cast<uint4*>(out + row[m][h] * p.n_res + col) = make_uint4(o[0], o[1], o[2], o[3]);
+          o[j] = pack_bf16x2(finish_bf16<EPI>(v[0][0], v[H - 1][0]), finish_bf16<EPI>(v[0][1], v[H - 1][1]));
         }
+        *reinterpret_cast<uint4*>(out + row[h] * p.n_res + col) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
@@ -539,8 +657,7 @@ int tile_rows(const AdapterShape& s) {
   if (!s.bf16) return kF32Rows;
   const int64_t pairs = (int64_t)s.E * std::min<int64_t>(s.N, s.T);
   const int64_t per_pair = s.rows / std::max<int64_t>(1, pairs);
-  const int most = s.r <= 32 ? 64 : s.r <= 64 ? 32 : 16;
-  return per_pair >= 48 ? most : per_pair >= 24 ? std::min(32, most) : 16;
+  return per_pair >= 24 && s.r <= 64 ? 32 : 16;
 }
 
 int64_t tiles_guess(const AdapterShape& s) {  // a likely number of tiles, for the grids only
@@ -576,19 +693,22 @@ PlanLayout layout(const AdapterShape& s) {
   return l;
 }
 
+template <typename K>
+cudaError_t allow_smem(K kernel, int smem) {
+  return smem <= 48 * 1024 ? cudaSuccess
+                           : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
 template <int MT, int RT>
 cudaError_t run_shrink(const ShrinkParams& p, dim3 grid, bool chained, cudaStream_t stream) {
-  return launch_maybe_chained(adapter_shrink_kernel<MT, RT>, grid, dim3(kThreads), 0, stream, chained, p);
+  const cudaError_t e = allow_smem(adapter_shrink_kernel<MT, RT>, shrink_smem<MT, RT>());
+  if (e != cudaSuccess) return e;
+  return launch_maybe_chained(adapter_shrink_kernel<MT, RT>, grid, dim3(kThreads), shrink_smem<MT, RT>(), stream, chained, p);
 }
 
 cudaError_t launch_shrink(const ShrinkParams& p, int tm, bool bf16, dim3 grid, bool chained, cudaStream_t stream) {
   if (!bf16)
     return launch_maybe_chained(adapter_shrink_f32_kernel, grid, dim3(kThreads), 0, stream, chained, p);
-  if (tm == 64) {
-    if (p.r <= 8) return run_shrink<4, 1>(p, grid, chained, stream);
-    if (p.r <= 16) return run_shrink<4, 2>(p, grid, chained, stream);
-    return run_shrink<4, 4>(p, grid, chained, stream);
-  }
   if (tm == 32) {
     if (p.r <= 8) return run_shrink<2, 1>(p, grid, chained, stream);
     if (p.r <= 16) return run_shrink<2, 2>(p, grid, chained, stream);
@@ -602,28 +722,28 @@ cudaError_t launch_shrink(const ShrinkParams& p, int tm, bool bf16, dim3 grid, b
   return run_shrink<1, 16>(p, grid, chained, stream);
 }
 
-template <int MT, int RK, int EPI>
+template <int WR, int RK, int EPI>
 cudaError_t run_expand(const ExpandParams& p, dim3 grid, cudaStream_t stream) {
-  return launch_maybe_chained(adapter_expand_kernel<MT, RK, EPI>, grid, dim3(kThreads), 0, stream, true, p);
+  const int smem = expand_smem<RK, EPI>();
+  const cudaError_t e = allow_smem(adapter_expand_kernel<WR, RK, EPI>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_maybe_chained(adapter_expand_kernel<WR, RK, EPI>, grid, dim3(kThreads), smem, stream, true, p);
+}
+
+template <int WR, int EPI>
+cudaError_t launch_expand_r(const ExpandParams& p, dim3 grid, cudaStream_t stream) {
+  if (p.r <= 16) return run_expand<WR, 1, EPI>(p, grid, stream);
+  if (p.r <= 32) return run_expand<WR, 2, EPI>(p, grid, stream);
+  if (p.r <= 64) return run_expand<WR, 4, EPI>(p, grid, stream);
+  return run_expand<WR, 8, EPI>(p, grid, stream);
 }
 
 template <int EPI>
 cudaError_t launch_expand(const ExpandParams& p, int tm, bool bf16, dim3 grid, cudaStream_t stream) {
   if (!bf16)
     return launch_maybe_chained(adapter_expand_f32_kernel<EPI>, grid, dim3(kThreads), 0, stream, true, p);
-  if (tm == 64) {
-    if (p.r <= 16) return run_expand<4, 1, EPI>(p, grid, stream);
-    return run_expand<4, 2, EPI>(p, grid, stream);
-  }
-  if (tm == 32) {
-    if (p.r <= 16) return run_expand<2, 1, EPI>(p, grid, stream);
-    if (p.r <= 32) return run_expand<2, 2, EPI>(p, grid, stream);
-    return run_expand<2, 4, EPI>(p, grid, stream);
-  }
-  if (p.r <= 16) return run_expand<1, 1, EPI>(p, grid, stream);
-  if (p.r <= 32) return run_expand<1, 2, EPI>(p, grid, stream);
-  if (p.r <= 64) return run_expand<1, 4, EPI>(p, grid, stream);
-  return run_expand<1, 8, EPI>(p, grid, stream);
+  if (tm == 32) return launch_expand_r<2, EPI>(p, grid, stream);
+  return launch_expand_r<1, EPI>(p, grid, stream);
 }
 
 }  // namespace
@@ -640,7 +760,7 @@ cudaError_t launch_adapter_plan(const AdapterShape& s, const int32_t* offsets, c
                reinterpret_cast<int32_t*>(base + l.order), reinterpret_cast<Tile*>(base + l.tiles),
                reinterpret_cast<int*>(base + kAdapterTilesAt), status};
   const unsigned blocks = (unsigned)((s.rows + kChunkRows - 1) / kChunkRows);
-  return launch_maybe_chained(adapter_plan_kernel, dim3(blocks), dim3(kChunkRows), sizeof(int) * (size_t)(s.E + 1),
+  return launch_maybe_chained(adapter_plan_kernel, dim3(blocks), dim3(kPlanThreads), sizeof(int) * (size_t)(s.E + 1),
                               stream, chained, p);
 }
 
@@ -664,10 +784,10 @@ cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, b
   cudaError_t e = launch_shrink(sp, tm, s.bf16, dim3(tiles_grid, (unsigned)S), chained, stream);
   if (e != cudaSuccess) return e;
   // columns per block: one round of the warps, more where there are enough tiles to fill the SMs
-  constexpr int kRound = 32 * kWarps;
+  const int kRound = 32 * kWarps / (s.bf16 ? tm / 16 : 1);
   const int64_t rounds = (n_res + kRound - 1) / kRound;
   const int64_t per = std::max<int64_t>(1, std::min<int64_t>(rounds, rounds * guess / (148 * 8)));
-  const int col_block = (int)std::min<int64_t>(per, 8) * kRound;
+  const int col_block = (int)std::min<int64_t>(per, 16) * kRound;
   ExpandParams ep{u, a.b, a.scale, a.base, a.out, order, tiles, n_tiles, s.rows, s.r, s.E, S, n_out, n_res, col_block,
                   !a.gate_up && a.base == a.out};
   const dim3 grid((unsigned)((n_res + col_block - 1) / col_block), tiles_grid);

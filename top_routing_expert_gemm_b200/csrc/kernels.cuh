@@ -189,6 +189,7 @@ struct AdapterApply {
   void* out;              // [rows, f or d]
   void* plan;
 };
+constexpr int64_t kAdapterMaxPairs = (int64_t(1) << 23) - 3;  // experts x adapters
 constexpr size_t kAdapterTilesAt = 64;  // byte offset of the tile count in the plan's header
 size_t adapter_plan_bytes(const AdapterShape& s);
 // The plan's header (kAdapterHeader bytes) has to be zero; status: where a bad

@@ -242,6 +242,7 @@ moe_status check_adapter_config(const moe_config* c, const moe_adapter_config* a
     return MOE_ERR_INVALID_ARG;
   if (ad->shared && c->n_shared == 0) return MOE_ERR_INVALID_ARG;
   if (ad->n_adapters > 65536 || ad->rank > 128) return MOE_ERR_UNSUPPORTED;
+  if (!ad->shared && (int64_t)c->n_experts * ad->n_adapters > kAdapterMaxPairs) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
