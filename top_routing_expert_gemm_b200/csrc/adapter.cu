@@ -6,7 +6,7 @@
 // of "Mixture of Experts Explained: Routers, Active Parameters and VRAM".
 //
 // Three kernels:
-//   plan    groups the rows of equal (expert, adapter) into tiles of up to TM
+//   plan    groups the rows of equal (expert, adapter) into tiles of up to 16
 //           rows: chunks of 256 rows are sorted inside a block, so no global
 //           sort and no histogram over the pairs is needed
 //   shrink  U = A x per tile, the reduction over the inputs split over S
@@ -26,11 +26,16 @@
 #include "common.cuh"
 #include "kernels.cuh"
 #include "pdl.cuh"
+#include "tc_primitives.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kChunkRows = 256;  // rows a plan block sorts
+// Rows of a tile: one MMA tile.  Tiles of 32 rows (half the reads of A and B
+// from L2) left too many of them half empty: the expand of the 2048-token
+// batch of 12 requests took 100 us with them, 87 us with 16 rows.
+constexpr int kTileRows = 16;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kFull = 0xffffffffu;
@@ -50,7 +55,7 @@ struct PlanParams {
   const int32_t* perm;     // [rows] or null: row = token
   const int32_t* token_adapter;
   int64_t rows;
-  int E, k, N, TM;
+  int E, k, N;
   int32_t* order;
   Tile* tiles;
   int* n_tiles;
@@ -121,7 +126,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
   }
   __syncthreads();
   // position tid of the sorted chunk starts a tile where its run starts, and
-  // every TM rows from there
+  // every kTileRows from there
   const int mine = tid < kChunkRows ? sorted[tid] : kSkip;
   bool head = false;
   int end = 0;
@@ -132,10 +137,10 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
       if (sorted[mid] < mine) lo = mid + 1;
       else hi = mid;
     }
-    head = (tid - lo) % p.TM == 0;
+    head = (tid - lo) % kTileRows == 0;
     if (head) {
       lo = tid + 1;
-      hi = min(kChunkRows, tid + p.TM);
+      hi = min(kChunkRows, tid + kTileRows);
       while (lo < hi) {  // first position behind the tile
         const int mid = (lo + hi) >> 1;
         if (sorted[mid] == mine) lo = mid + 1;
@@ -184,16 +189,11 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(static_cast<const uint4*>(p)); }
-
 // Asynchronous copies into the warp's own ring in shared memory: a lane reads
 // back only what it copied itself, so a wait_group is all the synchronisation
 // there is.  Without `on` the destination is zeroed and nothing is read.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -203,28 +203,29 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 // leave each of their warps (13.5 KiB), one stage at least, four at most
 constexpr int ring_stages(int bytes) { return bytes * 4 <= 13824 ? 4 : bytes * 3 <= 13824 ? 3 : bytes * 2 <= 13824 ? 2 : 1; }
 
-// MT row tiles of 16, up to RT rank tiles of 8.  A lane takes 8 consecutive
-// inputs of a row with one 16-byte load and uses them as the k indices 2t,
-// 2t+1, 2t+8, 2t+9 of two instructions: the sum runs over all inputs, so any
-// assignment of inputs to k serves as long as x and A agree.
+// 16 rows, up to RT rank tiles of 8.  A lane takes 8 consecutive inputs of a
+// row with one 16-byte copy and uses them as the k indices 2t, 2t+1, 2t+8, 2t+9
+// of two instructions: the sum runs over all inputs, so any assignment of inputs
+// to k serves as long as x and A agree.  The warps of a block take 64 inputs each
+// in turn and are added up at the end.
 constexpr int kUnit = 64;  // inputs per warp and round: whole 128-byte lines of every row
-template <int MT, int RT>
-constexpr int shrink_stage() { return 2 * (2 * MT + RT) * 512; }
-template <int MT, int RT>
+template <int RT>
+constexpr int shrink_stage() { return 2 * (2 + RT) * 512; }
+template <int RT>
 constexpr int shrink_smem() {
-  const int ring = kWarps * ring_stages(shrink_stage<MT, RT>()) * shrink_stage<MT, RT>();
-  const int red = kWarps / 2 * MT * 16 * RT * 8 * 4;  // the fold of the warps' sums, over the drained rings
+  const int ring = kWarps * ring_stages(shrink_stage<RT>()) * shrink_stage<RT>();
+  const int red = kWarps / 2 * 16 * RT * 8 * 4;  // the fold of the warps' sums, over the drained rings
   return ring > red ? ring : red;
 }
-template <int MT, int RT>
-__global__ void __launch_bounds__(kThreads, MT * RT <= 8 ? 2 : 1) adapter_shrink_kernel(const ShrinkParams p) {
-  constexpr int kStage = shrink_stage<MT, RT>(), kStages = ring_stages(kStage);
+template <int RT>
+__global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) adapter_shrink_kernel(const ShrinkParams p) {
+  constexpr int kStage = shrink_stage<RT>(), kStages = ring_stages(kStage);
   extern __shared__ __align__(16) uint8_t smem[];
-  float(*red)[MT * 16 * RT * 8] = reinterpret_cast<float(*)[MT * 16 * RT * 8]>(smem);
-  uint8_t* ring_ptr = smem + threadIdx.x / 32 * (kStages * kStage) + threadIdx.x % 32 * 16;
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_ptr);
+  float(*red)[16 * RT * 8] = reinterpret_cast<float(*)[16 * RT * 8]>(smem);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int g = lane / 4, t4 = lane % 4;
+  uint8_t* ring_ptr = smem + warp * (kStages * kStage) + lane * 16;
+  const uint32_t ring = tc::smem_u32(ring_ptr);
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   const int n_tiles = *p.n_tiles;
@@ -235,21 +236,14 @@ __global__ void __launch_bounds__(kThreads, MT * RT <= 8 ? 2 : 1) adapter_shrink
     if (tile.adapter < 0) continue;
     const __nv_bfloat16* a =
         static_cast<const __nv_bfloat16*>(p.a) + ((int64_t)tile.adapter * p.E + tile.expert) * p.r * p.K;
-    int64_t row[MT][2];
+    int64_t row[2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int h = 0; h < 2; ++h) row[h] = h * 8 + g < tile.count ? p.order[tile.start + h * 8 + g] : -1;
+    float acc[RT][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = m * 16 + h * 8 + g;
-        row[m][h] = i < tile.count ? p.order[tile.start + i] : -1;
-      }
-    float acc[MT][RT][4];
+    for (int n = 0; n < RT; ++n)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < RT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
 
     auto issue = [&](int k0, int slot) {
       const uint32_t dst = ring + slot * kStage;
@@ -263,12 +257,10 @@ __global__ void __launch_bounds__(kThreads, MT * RT <= 8 ? 2 : 1) adapter_shrink
           copy16(dst + (c * RT + n) * 512, on ? a + (int64_t)(n * 8 + g) * p.K + k : a, on);
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const bool on = in && row[m][h] >= 0;
-            copy16(dst + (2 * RT + (c * MT + m) * 2 + h) * 512, on ? x + row[m][h] * p.K + k : x, on);
-          }
+        for (int h = 0; h < 2; ++h) {
+          const bool on = in && row[h] >= 0;
+          copy16(dst + (2 * RT + c * 2 + h) * 512, on ? x + row[h] * p.K + k : x, on);
+        }
       }
     };
     const int k_first = k_lo + warp * kUnit;
@@ -286,17 +278,12 @@ __global__ void __launch_bounds__(kThreads, MT * RT <= 8 ? 2 : 1) adapter_shrink
       const uint4* st = reinterpret_cast<const uint4*>(ring_ptr + slot * kStage);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        uint4 av[RT];
+        const uint4 x0 = st[(2 * RT + c * 2) * 32], x1 = st[(2 * RT + c * 2 + 1) * 32];
 #pragma unroll
-        for (int n = 0; n < RT; ++n) av[n] = st[(c * RT + n) * 32];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint4 x0 = st[(2 * RT + (c * MT + m) * 2) * 32], x1 = st[(2 * RT + (c * MT + m) * 2 + 1) * 32];
-#pragma unroll
-          for (int n = 0; n < RT; ++n) {
-            mma_bf16(acc[m][n], x0.x, x1.x, x0.y, x1.y, av[n].x, av[n].y);
-            mma_bf16(acc[m][n], x0.z, x1.z, x0.w, x1.w, av[n].z, av[n].w);
-          }
+        for (int n = 0; n < RT; ++n) {
+          const uint4 av = st[(c * RT + n) * 32];
+          mma_bf16(acc[n], x0.x, x1.x, x0.y, x1.y, av.x, av.y);
+          mma_bf16(acc[n], x0.z, x1.z, x0.w, x1.w, av.z, av.w);
         }
       }
       if (++slot == kStages) slot = 0;
@@ -307,38 +294,32 @@ __global__ void __launch_bounds__(kThreads, MT * RT <= 8 ? 2 : 1) adapter_shrink
       __syncthreads();
       if (warp >= half && warp < 2 * half) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int n = 0; n < RT; ++n)
-            *reinterpret_cast<float4*>(&red[warp - half][((m * RT + n) * 32 + lane) * 4]) =
-                make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+        for (int n = 0; n < RT; ++n)
+          *reinterpret_cast<float4*>(&red[warp - half][(n * 32 + lane) * 4]) =
+              make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
       }
       __syncthreads();
       if (warp < half) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int n = 0; n < RT; ++n) {
-            const float4 o = *reinterpret_cast<const float4*>(&red[warp][((m * RT + n) * 32 + lane) * 4]);
-            acc[m][n][0] += o.x;
-            acc[m][n][1] += o.y;
-            acc[m][n][2] += o.z;
-            acc[m][n][3] += o.w;
-          }
+        for (int n = 0; n < RT; ++n) {
+          const float4 o = *reinterpret_cast<const float4*>(&red[warp][(n * 32 + lane) * 4]);
+          acc[n][0] += o.x;
+          acc[n][1] += o.y;
+          acc[n][2] += o.z;
+          acc[n][3] += o.w;
+        }
       }
     }
     if (warp == 0) {
       float* u = p.u + ((int64_t)blockIdx.y * p.rows + tile.start) * p.r;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < RT; ++n)
 #pragma unroll
-        for (int n = 0; n < RT; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int i = m * 16 + h * 8 + g, c = n * 8 + 2 * t4;
-            if (i < tile.count && c < p.r)
-              *reinterpret_cast<float2*>(u + (int64_t)i * p.r + c) = make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
-          }
+        for (int h = 0; h < 2; ++h) {
+          const int i = h * 8 + g, c = n * 8 + 2 * t4;
+          if (i < tile.count && c < p.r)
+            *reinterpret_cast<float2*>(u + (int64_t)i * p.r + c) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+        }
     }
     __syncthreads();  // the fold is read before the next tile's copies land there
   }
@@ -414,8 +395,11 @@ struct ExpandParams {
   int64_t rows;
   int r, E, S;
   int n_out, n_res;  // columns of base and of the result
-  int col_block;     // result columns per block (blockIdx.x), whole rounds of the block's warps
+  int col_block;     // fp32: result columns per block (blockIdx.x)
   bool in_place;     // base is the result and nothing is applied to it: rows without an adapter are right
+  int stages, stage_bytes;  // bf16: the ring
+  int* status;
+  uint64_t wait_limit_ns;
 };
 
 template <int EPI>
@@ -423,171 +407,277 @@ __device__ __forceinline__ float finish(float v, float up) {
   return EPI == kEpiSwiGLU ? silu_f(v) * up : EPI == kEpiGELU ? gelu_f(v) : v;
 }
 
-// SiLU for results that are rounded to bf16: __expf and __fdividef are off by
-// under 2^-19 of the value for any argument that leaves one above 2^-126,
-// against half a bf16 step of 2^-9; expf and the IEEE division made the kernel
-// issue bound (285 against 94 us for the 2048-token batch below).
-__device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+// SiLU for results that are rounded to bf16, z / (1 + 2^(-z log2 e)) with the
+// hardware's approximate exponential and reciprocal: their 2^-22 and the
+// argument's rounding (|z| 2^-24 of the exponential) are lost under half a bf16
+// step, 2^-9.  With expf and the IEEE division the kernel was issue bound.
+// Denormals are flushed: the results there are below 2^-119.
+__device__ __forceinline__ float silu_fast(float z) {
+  float e, q;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
+  return z * q;
+}
 
 template <int EPI>
 __device__ __forceinline__ float finish_bf16(float v, float up) {
   return EPI == kEpiSwiGLU ? silu_fast(v) * up : EPI == kEpiGELU ? gelu_f(v) : v;
 }
 
-// A warp takes 16 rows of the tile and 32 result columns (and, for SwiGLU, the
-// matching 32 up columns) per round; the block's warps cover the tile's WR row
-// groups side by side, so they share B through L1.  Column 2t+i of instruction
-// j stands for result column 8t + 2j + i, so a lane ends with 8 consecutive
-// columns of a row: base comes and the result leaves in 16-byte vectors.  U
-// enters as a sum of two bf16 values (16 bits of mantissa), so its rounding
-// does not show beside the result's own.
+// The work is a list of rounds: a tile times CW result columns (and, for
+// SwiGLU, the matching up columns), tile after tile; every block takes an equal
+// run of it, so the blocks end together whatever the tiles are.  A producer warp
+// fetches the columns' rows of B (one contiguous piece each) into a ring of
+// stages with bulk copies under mbarriers; eight consumer warps each take 32
+// columns of a round and fetch their part of base themselves, each lane its own 16-byte vectors, a few rounds ahead.  (base by
+// bulk copies as well, a segment of each row, measured 186 against 117 us for
+// 16-byte copies: at 256 bytes a bulk copy costs more than it moves.)
+//
+// Column 2t+i of instruction j stands for column 8t + 2j + i of the warp's 32, so
+// a lane ends with 8 consecutive columns of a row: base is read and the result
+// leaves in 16-byte vectors.  base is the accumulators' first value.  U enters
+// as a sum of two bf16 values (16 bits of mantissa), so its rounding does not
+// show beside the result's own.
+constexpr int kMaxStages = 8;
+struct ExpandHeader {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  int fill_par[kMaxStages];
+  int abort;
+};
+constexpr int kExpandHead = 256;
+static_assert(sizeof(ExpandHeader) <= kExpandHead, "header of the expand ring");
+constexpr int kExpandThreads = kThreads + 32;
+
+template <int EPI>
+struct ExpandShape {
+  static constexpr int H = EPI == kEpiSwiGLU ? 2 : 1;
+  static constexpr int CW = 32 * kWarps;        // result columns of a round
+  static constexpr int kAhead = 4;              // rounds of base in flight per warp, the current one included
+  static constexpr int kSlot = 2 * H * 512;     // a warp's part of base
+  static constexpr int kBase = kWarps * kAhead * kSlot;
+  static int stage_bytes(int r) { return H * CW * r * 2; }
+};
+
+// Blocks per SM that the registers (and, below, the rings) leave room for
 template <int RK, int EPI>
-constexpr int expand_stage() { return (EPI == kEpiSwiGLU ? 2 : 1) * (2 * 512 + 4 * RK * 256); }
+constexpr int expand_blocks() { return RK > 2 ? 1 : RK == 1 && EPI != kEpiSwiGLU ? 3 : 2; }
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, int bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 template <int RK, int EPI>
-constexpr int expand_smem() { return kWarps * ring_stages(expand_stage<RK, EPI>()) * expand_stage<RK, EPI>(); }
-template <int WR, int RK, int EPI>
-__global__ void __launch_bounds__(kThreads, RK <= 2 ? 2 : 1) adapter_expand_kernel(const ExpandParams p) {
-  constexpr int H = EPI == kEpiSwiGLU ? 2 : 1;
-  constexpr int kStage = expand_stage<RK, EPI>(), kStages = ring_stages(kStage);
-  constexpr int kB = 2 * H * 512;  // base first, then B
+__global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>()) adapter_expand_kernel(const ExpandParams p) {
+  using Sh = ExpandShape<EPI>;
+  constexpr int H = Sh::H, CW = Sh::CW;
   extern __shared__ __align__(16) uint8_t smem[];
-  uint8_t* ring_ptr = smem + threadIdx.x / 32 * (kStages * kStage);
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_ptr);
-  constexpr int CG = kWarps / WR;  // column groups of a round
+  ExpandHeader* hd = reinterpret_cast<ExpandHeader*>(smem);
+  uint8_t* ring = smem + kExpandHead + Sh::kBase;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int g = lane / 4, t4 = lane % 4;
-  const int i0 = warp % WR * 16;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      tc::mbar_init(tc::smem_u32(&hd->full[i]), 1);
+      tc::mbar_init(tc::smem_u32(&hd->empty[i]), kWarps);
+      hd->fill_par[i] = -1;
+    }
+    hd->abort = 0;
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
-  const int n_tiles = *p.n_tiles;
-  const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.base);
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-  for (int t = blockIdx.y; t < n_tiles; t += gridDim.y) {
-    const Tile tile = p.tiles[t];
-    const bool has = tile.adapter >= 0;
-    if ((!has && p.in_place) || i0 >= tile.count) continue;
-    int64_t row[2];
+  volatile int* abort_flag = &hd->abort;
+  const int rounds = (p.n_res + CW - 1) / CW;  // per tile
+  const int64_t total = (int64_t)*p.n_tiles * rounds;
+  const int64_t lo_round = total * blockIdx.x / gridDim.x, hi_round = total * (blockIdx.x + 1) / gridDim.x;
+  const int b_bytes = CW * p.r * 2;
+  int stage = 0;
+  uint32_t phase = 0;
+
+  if (warp == kWarps) {
+    // ------------------------------------------------ producer (one lane)
+    if (lane == 0) {
+      bool ok = true;
+      for (int64_t at = lo_round; ok && at < hi_round;) {
+        const Tile tile = p.tiles[at / rounds];
+        int q = (int)(at % rounds);
+        const int q_end = (int)min((int64_t)rounds, q + (hi_round - at));
+        at += q_end - q;
+        if (tile.adapter < 0) continue;
+        const __nv_bfloat16* b =
+            static_cast<const __nv_bfloat16*>(p.b) + ((int64_t)tile.adapter * p.E + tile.expert) * p.n_out * p.r;
+        for (; q < q_end; ++q) {
+          const int c0 = q * CW, cols = min(CW, p.n_res - c0);
+          const uint32_t full = tc::smem_u32(&hd->full[stage]);
+          ok = tc::mbar_wait_bounded(tc::smem_u32(&hd->empty[stage]), phase ^ 1u, abort_flag, p.wait_limit_ns,
+                                     p.status);
+          if (!ok) break;
+          tc::mbar_expect_tx(full, H * cols * p.r * 2);
+          hd->fill_par[stage] = (int)phase;
+          const uint32_t dst = tc::smem_u32(ring + stage * p.stage_bytes);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) row[h] = i0 + h * 8 + g < tile.count ? p.order[tile.start + i0 + h * 8 + g] : -1;
-    const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(p.b) +
-                             ((int64_t)(has ? tile.adapter : 0) * p.E + tile.expert) * p.n_out * p.r;
-    const int c_first = blockIdx.x * p.col_block + warp / WR * 32;
-    const int c_end = min(p.n_res, (int)((blockIdx.x + 1) * p.col_block));
-    auto issue = [&](int c0, int slot) {
-      const int col = c0 + 8 * t4;  // this lane's 8 result columns
-      const uint32_t dst = ring + slot * kStage;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int q = 0; q < H; ++q) {
-          const bool on = col < p.n_res && row[h] >= 0;
-          copy16(dst + (h * H + q) * 512 + lane * 16, on ? base + row[h] * p.n_out + q * p.n_res + col : base, on);
-        }
-#pragma unroll
-      for (int q = 0; q < H; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = c0 + 8 * (g / 2) + 2 * j + (g & 1);
-#pragma unroll
-          for (int c = 0; c < RK; ++c) {
-            const int k = 16 * c + 4 * t4;
-            const bool on = has && n < p.n_res && k < p.r;
-            copy8(dst + kB + ((q * 4 + j) * RK + c) * 256 + lane * 8,
-                  on ? b + (int64_t)(q * p.n_res + n) * p.r + k : base, on);
+          for (int h = 0; h < H; ++h)
+            bulk_copy(dst + h * b_bytes, b + (int64_t)(h * p.n_res + c0) * p.r, cols * p.r * 2, full);
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
           }
         }
-    };
-#pragma unroll
-    for (int d = 0; d < kStages - 1; ++d) {
-      if (c_first + d * CG * 32 < c_end) issue(c_first + d * CG * 32, d);
-      copies_commit();
-    }
-    uint32_t hi[RK][4], lo[RK][4];  // U fragments: rows g, g+8; ranks 16 c + 4 t4 + {0,1} and {2,3}
-    const float sc = has ? p.scale[tile.adapter] : 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int c = 0; c < RK; ++c) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int k = 16 * c + 4 * t4;
-        if (has && row[h] >= 0 && k < p.r) {
-          const float* u = p.u + (int64_t)(tile.start + i0 + h * 8 + g) * p.r + k;
-#pragma unroll 4
-          for (int s = 0; s < p.S; ++s) {
-            const float4 w = __ldg(reinterpret_cast<const float4*>(u + (int64_t)s * p.rows * p.r));
-            v.x += w.x;
-            v.y += w.y;
-            v.z += w.z;
-            v.w += w.w;
-          }
-          v = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
-        }
-        hi[c][h] = pack_bf16x2(v.x, v.y);
-        hi[c][2 + h] = pack_bf16x2(v.z, v.w);
-        const __nv_bfloat162 p0 = *reinterpret_cast<__nv_bfloat162*>(&hi[c][h]);
-        const __nv_bfloat162 p1 = *reinterpret_cast<__nv_bfloat162*>(&hi[c][2 + h]);
-        lo[c][h] = pack_bf16x2(v.x - __low2float(p0), v.y - __high2float(p0));
-        lo[c][2 + h] = pack_bf16x2(v.z - __low2float(p1), v.w - __high2float(p1));
       }
     }
-    int slot = 0;
-    for (int c0 = c_first; c0 < c_end; c0 += CG * 32) {
-      const int ahead = c0 + (kStages - 1) * CG * 32;
-      if (ahead < c_end) issue(ahead, slot == 0 ? kStages - 1 : slot - 1);
-      copies_commit();
-      copies_wait<kStages - 1>();
-      const int col = c0 + 8 * t4;
-      const bool in = col < p.n_res;
-      const uint8_t* st = ring_ptr + slot * kStage;
-      const uint4* st_base = reinterpret_cast<const uint4*>(st) + lane;
-      const uint2* st_b = reinterpret_cast<const uint2*>(st + kB) + lane;
-      if (++slot == kStages) slot = 0;
-      float acc[H][4][4];
+  } else {
+    // ------------------------------------------------ consumers
+    const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.base);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+    const int g = lane / 4, t4 = lane % 4;
+    const int w0 = warp * 32;  // this warp's columns of a round
+    const uint8_t* mine = smem + kExpandHead + warp * (Sh::kAhead * Sh::kSlot) + lane * 16;
+    const uint32_t mine32 = tc::smem_u32(mine);
+    bool ok = true;
+    for (int64_t at = lo_round; ok && at < hi_round;) {
+      const Tile tile = p.tiles[at / rounds];
+      const int q0 = (int)(at % rounds);
+      const int q_end = (int)min((int64_t)rounds, q0 + (hi_round - at));
+      at += q_end - q0;
+      const bool has = tile.adapter >= 0;
+      if (!has && p.in_place) continue;
+      __nv_bfloat16* orow[2];
+      const __nv_bfloat16* src[2][H];  // this lane's vectors of the next round to fetch
+      bool on[2];
 #pragma unroll
-      for (int q = 0; q < H; ++q)
+      for (int i = 0; i < 2; ++i) {
+        on[i] = i * 8 + g < tile.count;
+        const int64_t row = on[i] ? p.order[tile.start + i * 8 + g] : 0;
+        orow[i] = out + row * p.n_res + w0 + 8 * t4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float(&d)[4] = acc[q][j];
-          d[0] = d[1] = d[2] = d[3] = 0.f;
+        for (int h = 0; h < H; ++h) src[i][h] = base + row * p.n_out + h * p.n_res + q0 * CW + w0 + 8 * t4;
+      }
+      auto issue = [&](int q, int slot) {
+        const bool in = q * CW + w0 + 8 * t4 < p.n_res;
 #pragma unroll
-          for (int c = 0; c < RK; ++c) {
-            const uint2 bv = st_b[((q * 4 + j) * RK + c) * 32];
-            mma_bf16(d, lo[c][0], lo[c][1], lo[c][2], lo[c][3], bv.x, bv.y);
-            mma_bf16(d, hi[c][0], hi[c][1], hi[c][2], hi[c][3], bv.x, bv.y);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            copy16(mine32 + slot * Sh::kSlot + (i * H + h) * 512, src[i][h], in && on[i]);
+            src[i][h] += CW;
           }
-        }
+      };
+#pragma unroll
+      for (int d = 0; d < Sh::kAhead - 1; ++d) {
+        if (q0 + d < q_end) issue(q0 + d, d);
+        copies_commit();
+      }
+      uint32_t hi[RK][4], lo[RK][4];  // U fragments: rows g, g+8; ranks 16 c + 4 t4 + {0,1} and {2,3}
+      const float sc = has ? p.scale[tile.adapter] : 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (!in || row[h] < 0) continue;
-        uint4 bs[H];
 #pragma unroll
-        for (int q = 0; q < H; ++q) bs[q] = st_base[(h * H + q) * 32];
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v[H][2];
-#pragma unroll
-          for (int q = 0; q < H; ++q) {
-            const uint32_t w = j == 0 ? bs[q].x : j == 1 ? bs[q].y : j == 2 ? bs[q].z : bs[q].w;
-            v[q][0] = __uint_as_float(w << 16) + acc[q][j][2 * h];
-            v[q][1] = __uint_as_float(w & 0xffff0000u) + acc[q][j][2 * h + 1];
+        for (int c = 0; c < RK; ++c) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          const int k = 16 * c + 4 * t4;
+          if (has && on[h] && k < p.r) {
+            const float* u = p.u + (int64_t)(tile.start + h * 8 + g) * p.r + k;
+#pragma unroll 4
+            for (int s = 0; s < p.S; ++s) {
+              const float4 w = __ldg(reinterpret_cast<const float4*>(u + (int64_t)s * p.rows * p.r));
+              v.x += w.x;
+              v.y += w.y;
+              v.z += w.z;
+              v.w += w.w;
+            }
+            v = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
           }
-          o[j] = pack_bf16x2(finish_bf16<EPI>(v[0][0], v[H - 1][0]), finish_bf16<EPI>(v[0][1], v[H - 1][1]));
+          hi[c][h] = pack_bf16x2(v.x, v.y);
+          hi[c][2 + h] = pack_bf16x2(v.z, v.w);
+          const __nv_bfloat162 p0 = *reinterpret_cast<__nv_bfloat162*>(&hi[c][h]);
+          const __nv_bfloat162 p1 = *reinterpret_cast<__nv_bfloat162*>(&hi[c][2 + h]);
+          lo[c][h] = pack_bf16x2(v.x - __low2float(p0), v.y - __high2float(p0));
+          lo[c][2 + h] = pack_bf16x2(v.z - __low2float(p1), v.w - __high2float(p1));
         }
-        *reinterpret_cast<uint4*>(out + row[h] * p.n_res + col) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      int slot = 0;
+      for (int q = q0; q < q_end; ++q) {
+        if (q + Sh::kAhead - 1 < q_end) issue(q + Sh::kAhead - 1, (slot + Sh::kAhead - 1) % Sh::kAhead);
+        copies_commit();
+        copies_wait<Sh::kAhead - 1>();
+        const int c0 = q * CW;
+        const bool work = c0 + w0 < p.n_res;
+        float acc[H][4][4];
+        if (work) {
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            const uint4 r0 = *reinterpret_cast<const uint4*>(mine + slot * Sh::kSlot + h * 512);
+            const uint4 r1 = *reinterpret_cast<const uint4*>(mine + slot * Sh::kSlot + (H + h) * 512);
+            const uint32_t w[2][4] = {{r0.x, r0.y, r0.z, r0.w}, {r1.x, r1.y, r1.z, r1.w}};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                acc[h][j][2 * i] = __uint_as_float(w[i][j] << 16);
+                acc[h][j][2 * i + 1] = __uint_as_float(w[i][j] & 0xffff0000u);
+              }
+          }
+        }
+        slot = (slot + 1) % Sh::kAhead;
+        if (has) {
+          ok = tc::mbar_wait_bounded(tc::smem_u32(&hd->full[stage]), phase, abort_flag, p.wait_limit_ns, p.status);
+          if (!ok) break;
+          if (work) {
+            const uint8_t* st = ring + stage * p.stage_bytes + (w0 + 8 * (g / 2) + (g & 1)) * p.r * 2 + 8 * t4;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint8_t* sb = st + h * b_bytes + j * 4 * p.r;
+#pragma unroll
+                for (int c = 0; c < RK; ++c) {
+                  const uint2 bv = 16 * c + 4 * t4 < p.r ? *reinterpret_cast<const uint2*>(sb + 32 * c) : make_uint2(0, 0);
+                  mma_bf16(acc[h][j], lo[c][0], lo[c][1], lo[c][2], lo[c][3], bv.x, bv.y);
+                  mma_bf16(acc[h][j], hi[c][0], hi[c][1], hi[c][2], hi[c][3], bv.x, bv.y);
+                }
+              }
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&hd->empty[stage]));
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (work && c0 + w0 + 8 * t4 < p.n_res) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!on[i]) continue;
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              o[j] = pack_bf16x2(finish_bf16<EPI>(acc[0][j][2 * i], acc[H - 1][j][2 * i]),
+                                 finish_bf16<EPI>(acc[0][j][2 * i + 1], acc[H - 1][j][2 * i + 1]));
+            *reinterpret_cast<uint4*>(orow[i] + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
       }
     }
   }
+  copies_wait<0>();  // an aborted round may have left some
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) {
+    // let the copies in flight land before the block's shared memory goes
+    for (int i = 0; i < p.stages; ++i)
+      if (hd->fill_par[i] >= 0) tc::drain_wait(tc::smem_u32(&hd->full[i]), (uint32_t)hd->fill_par[i]);
+  }
+  __syncthreads();
 }
 
 // fp32: a thread takes one result column of the tile's (at most 16) rows; U
 // is broadcast from shared memory
-constexpr int kF32Rows = 16;
 template <int EPI>
 __global__ void __launch_bounds__(kThreads) adapter_expand_f32_kernel(const ExpandParams p) {
   constexpr int H = EPI == kEpiSwiGLU ? 2 : 1;
-  __shared__ __align__(16) float su[kF32Rows][128];
-  __shared__ int srow[kF32Rows];
+  __shared__ __align__(16) float su[kTileRows][128];
+  __shared__ int srow[kTileRows];
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   const int n_tiles = *p.n_tiles;
@@ -598,7 +688,7 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_f32_kernel(const Expa
     const bool has = tile.adapter >= 0;
     if (!has && p.in_place) continue;
     __syncthreads();
-    for (int i = threadIdx.x; i < kF32Rows * p.r; i += kThreads) {
+    for (int i = threadIdx.x; i < kTileRows * p.r; i += kThreads) {
       const int rr = i / p.r, k = i % p.r;
       float v = 0.f;
       if (has && rr < tile.count) {
@@ -613,9 +703,9 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_f32_kernel(const Expa
     const float* b = static_cast<const float*>(p.b) + ((int64_t)(has ? tile.adapter : 0) * p.E + tile.expert) * p.n_out * p.r;
     const int c_end = min(p.n_res, (int)((blockIdx.x + 1) * p.col_block));
     for (int col = blockIdx.x * p.col_block + threadIdx.x; col < c_end; col += kThreads) {
-      float acc[kF32Rows][H];
+      float acc[kTileRows][H];
 #pragma unroll
-      for (int i = 0; i < kF32Rows; ++i)
+      for (int i = 0; i < kTileRows; ++i)
 #pragma unroll
         for (int q = 0; q < H; ++q) acc[i][q] = 0.f;
       if (has) {
@@ -625,7 +715,7 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_f32_kernel(const Expa
           for (int q = 0; q < H; ++q)
             bv[q] = __ldg(reinterpret_cast<const float4*>(b + (int64_t)(q * p.n_res + col) * p.r + k));
 #pragma unroll
-          for (int i = 0; i < kF32Rows; ++i) {
+          for (int i = 0; i < kTileRows; ++i) {
             const float4 uv = *reinterpret_cast<const float4*>(&su[i][k]);
 #pragma unroll
             for (int q = 0; q < H; ++q) {
@@ -638,7 +728,7 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_f32_kernel(const Expa
         }
       }
 #pragma unroll
-      for (int i = 0; i < kF32Rows; ++i) {
+      for (int i = 0; i < kTileRows; ++i) {
         if (i >= tile.count) break;
         const int64_t row = srow[i];
         float v[H];
@@ -651,19 +741,9 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_f32_kernel(const Expa
 }
 
 // ---------------------------------------------------------------- host side
-// Rows of a tile: 16 (one MMA tile) where a pair has few rows or the rank's
-// accumulators leave no room, more where the reuse of A and B pays
-int tile_rows(const AdapterShape& s) {
-  if (!s.bf16) return kF32Rows;
-  const int64_t pairs = (int64_t)s.E * std::min<int64_t>(s.N, s.T);
-  const int64_t per_pair = s.rows / std::max<int64_t>(1, pairs);
-  return per_pair >= 24 && s.r <= 64 ? 32 : 16;
-}
-
 int64_t tiles_guess(const AdapterShape& s) {  // a likely number of tiles, for the grids only
-  const int tm = tile_rows(s);
   const int64_t pairs = std::min<int64_t>(s.rows, (int64_t)s.E * std::min<int64_t>(s.N, s.T));
-  return std::max<int64_t>(1, std::min<int64_t>(s.rows, s.rows / tm + pairs));
+  return std::max<int64_t>(1, std::min<int64_t>(s.rows, s.rows / kTileRows + pairs));
 }
 
 // Blocks that share one reduction of K inputs, and the inputs of each: enough
@@ -699,51 +779,57 @@ cudaError_t allow_smem(K kernel, int smem) {
                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
-template <int MT, int RT>
+template <int RT>
 cudaError_t run_shrink(const ShrinkParams& p, dim3 grid, bool chained, cudaStream_t stream) {
-  const cudaError_t e = allow_smem(adapter_shrink_kernel<MT, RT>, shrink_smem<MT, RT>());
+  const cudaError_t e = allow_smem(adapter_shrink_kernel<RT>, shrink_smem<RT>());
   if (e != cudaSuccess) return e;
-  return launch_maybe_chained(adapter_shrink_kernel<MT, RT>, grid, dim3(kThreads), shrink_smem<MT, RT>(), stream, chained, p);
+  return launch_maybe_chained(adapter_shrink_kernel<RT>, grid, dim3(kThreads), shrink_smem<RT>(), stream, chained, p);
 }
 
-cudaError_t launch_shrink(const ShrinkParams& p, int tm, bool bf16, dim3 grid, bool chained, cudaStream_t stream) {
+cudaError_t launch_shrink(const ShrinkParams& p, bool bf16, dim3 grid, bool chained, cudaStream_t stream) {
   if (!bf16)
     return launch_maybe_chained(adapter_shrink_f32_kernel, grid, dim3(kThreads), 0, stream, chained, p);
-  if (tm == 32) {
-    if (p.r <= 8) return run_shrink<2, 1>(p, grid, chained, stream);
-    if (p.r <= 16) return run_shrink<2, 2>(p, grid, chained, stream);
-    if (p.r <= 32) return run_shrink<2, 4>(p, grid, chained, stream);
-    return run_shrink<2, 8>(p, grid, chained, stream);
+  if (p.r <= 8) return run_shrink<1>(p, grid, chained, stream);
+  if (p.r <= 16) return run_shrink<2>(p, grid, chained, stream);
+  if (p.r <= 32) return run_shrink<4>(p, grid, chained, stream);
+  if (p.r <= 64) return run_shrink<8>(p, grid, chained, stream);
+  return run_shrink<16>(p, grid, chained, stream);
+}
+
+// As many blocks per SM as leave each a ring of two stages
+template <int RK, int EPI>
+cudaError_t run_expand(const ExpandParams& params, cudaStream_t stream) {
+  using Sh = ExpandShape<EPI>;
+  ExpandParams p = params;
+  p.stage_bytes = Sh::stage_bytes(p.r);
+  int per_sm = expand_blocks<RK, EPI>(), room = 0;
+  for (;; --per_sm) {
+    room = 227 * 1024 / per_sm - 1024 - kExpandHead - Sh::kBase;
+    if (per_sm == 1 || room >= 2 * p.stage_bytes) break;
   }
-  if (p.r <= 8) return run_shrink<1, 1>(p, grid, chained, stream);
-  if (p.r <= 16) return run_shrink<1, 2>(p, grid, chained, stream);
-  if (p.r <= 32) return run_shrink<1, 4>(p, grid, chained, stream);
-  if (p.r <= 64) return run_shrink<1, 8>(p, grid, chained, stream);
-  return run_shrink<1, 16>(p, grid, chained, stream);
-}
-
-template <int WR, int RK, int EPI>
-cudaError_t run_expand(const ExpandParams& p, dim3 grid, cudaStream_t stream) {
-  const int smem = expand_smem<RK, EPI>();
-  const cudaError_t e = allow_smem(adapter_expand_kernel<WR, RK, EPI>, smem);
+  p.stages = std::min(kMaxStages, room / p.stage_bytes);
+  const int smem = kExpandHead + Sh::kBase + p.stages * p.stage_bytes;
+  const cudaError_t e = allow_smem(adapter_expand_kernel<RK, EPI>, smem);
   if (e != cudaSuccess) return e;
-  return launch_maybe_chained(adapter_expand_kernel<WR, RK, EPI>, grid, dim3(kThreads), smem, stream, true, p);
-}
-
-template <int WR, int EPI>
-cudaError_t launch_expand_r(const ExpandParams& p, dim3 grid, cudaStream_t stream) {
-  if (p.r <= 16) return run_expand<WR, 1, EPI>(p, grid, stream);
-  if (p.r <= 32) return run_expand<WR, 2, EPI>(p, grid, stream);
-  if (p.r <= 64) return run_expand<WR, 4, EPI>(p, grid, stream);
-  return run_expand<WR, 8, EPI>(p, grid, stream);
+  const int64_t most = p.rows * ((p.n_res + Sh::CW - 1) / Sh::CW);  // rounds, if every row were a tile
+  const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)device_sm_count() * per_sm);
+  return launch_maybe_chained(adapter_expand_kernel<RK, EPI>, dim3(grid), dim3(kExpandThreads), smem, stream, true,
+                              p);
 }
 
 template <int EPI>
-cudaError_t launch_expand(const ExpandParams& p, int tm, bool bf16, dim3 grid, cudaStream_t stream) {
+cudaError_t launch_expand_r(const ExpandParams& p, cudaStream_t stream) {
+  if (p.r <= 16) return run_expand<1, EPI>(p, stream);
+  if (p.r <= 32) return run_expand<2, EPI>(p, stream);
+  if (p.r <= 64) return run_expand<4, EPI>(p, stream);
+  return run_expand<8, EPI>(p, stream);
+}
+
+template <int EPI>
+cudaError_t launch_expand(const ExpandParams& p, bool bf16, dim3 grid, cudaStream_t stream) {
   if (!bf16)
     return launch_maybe_chained(adapter_expand_f32_kernel<EPI>, grid, dim3(kThreads), 0, stream, true, p);
-  if (tm == 32) return launch_expand_r<2, EPI>(p, grid, stream);
-  return launch_expand_r<1, EPI>(p, grid, stream);
+  return launch_expand_r<EPI>(p, stream);
 }
 
 }  // namespace
@@ -756,7 +842,7 @@ cudaError_t launch_adapter_plan(const AdapterShape& s, const int32_t* offsets, c
   uint8_t* base = static_cast<uint8_t*>(plan);
   const PlanLayout l = layout(s);
   if (s.rows == 0) return cudaSuccess;
-  PlanParams p{offsets, perm, token_adapter, s.rows, s.E, s.k, s.N, tile_rows(s),
+  PlanParams p{offsets, perm, token_adapter, s.rows, s.E, s.k, s.N,
                reinterpret_cast<int32_t*>(base + l.order), reinterpret_cast<Tile*>(base + l.tiles),
                reinterpret_cast<int*>(base + kAdapterTilesAt), status};
   const unsigned blocks = (unsigned)((s.rows + kChunkRows - 1) / kChunkRows);
@@ -768,7 +854,6 @@ cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, b
   if (s.rows == 0) return cudaSuccess;
   uint8_t* base = static_cast<uint8_t*>(a.plan);
   const PlanLayout l = layout(s);
-  const int tm = tile_rows(s);
   const int K = a.gate_up ? s.d : s.f;
   const int n_res = a.gate_up ? s.f : s.d;
   const int n_out = a.gate_up && s.act == kEpiSwiGLU ? 2 * s.f : n_res;
@@ -781,19 +866,19 @@ cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, b
   const int64_t guess = tiles_guess(s);
   const unsigned tiles_grid = (unsigned)std::min<int64_t>(guess, 4096);
   ShrinkParams sp{a.x, a.a, order, tiles, n_tiles, u, s.rows, K, s.r, s.E, k_block};
-  cudaError_t e = launch_shrink(sp, tm, s.bf16, dim3(tiles_grid, (unsigned)S), chained, stream);
+  cudaError_t e = launch_shrink(sp, s.bf16, dim3(tiles_grid, (unsigned)S), chained, stream);
   if (e != cudaSuccess) return e;
-  // columns per block: one round of the warps, more where there are enough tiles to fill the SMs
-  const int kRound = 32 * kWarps / (s.bf16 ? tm / 16 : 1);
+  // fp32: one round of the block's threads, more where there are enough tiles to fill the SMs
+  constexpr int kRound = kThreads;
   const int64_t rounds = (n_res + kRound - 1) / kRound;
   const int64_t per = std::max<int64_t>(1, std::min<int64_t>(rounds, rounds * guess / (148 * 8)));
   const int col_block = (int)std::min<int64_t>(per, 16) * kRound;
   ExpandParams ep{u, a.b, a.scale, a.base, a.out, order, tiles, n_tiles, s.rows, s.r, s.E, S, n_out, n_res, col_block,
-                  !a.gate_up && a.base == a.out};
+                  !a.gate_up && a.base == a.out, 0, 0, a.status, a.wait_limit_ns};
   const dim3 grid((unsigned)((n_res + col_block - 1) / col_block), tiles_grid);
-  if (!a.gate_up) return launch_expand<kEpiNone>(ep, tm, s.bf16, grid, stream);
-  return s.act == kEpiSwiGLU ? launch_expand<kEpiSwiGLU>(ep, tm, s.bf16, grid, stream)
-                             : launch_expand<kEpiGELU>(ep, tm, s.bf16, grid, stream);
+  if (!a.gate_up) return launch_expand<kEpiNone>(ep, s.bf16, grid, stream);
+  return s.act == kEpiSwiGLU ? launch_expand<kEpiSwiGLU>(ep, s.bf16, grid, stream)
+                             : launch_expand<kEpiGELU>(ep, s.bf16, grid, stream);
 }
 
 }  // namespace moe

@@ -188,6 +188,8 @@ struct AdapterApply {
   const void* base;       // [rows, outputs]
   void* out;              // [rows, f or d]
   void* plan;
+  int* status;            // where an expired wait is reported
+  uint64_t wait_limit_ns;
 };
 constexpr int64_t kAdapterMaxPairs = (int64_t(1) << 23) - 3;  // experts x adapters
 constexpr size_t kAdapterTilesAt = 64;  // byte offset of the tile count in the plan's header

@@ -268,7 +268,8 @@ moe_status adapter_apply(const moe_config* cfg, const moe_adapter_config* ad, bo
   DeviceGuard g;
   if ((st = enter(g, plan, stream)) != MOE_OK) return st;
   if ((st = g.same_device(out)) != MOE_OK) return st;
-  MOE_CUDA_TRY(launch_adapter_apply(s, AdapterApply{gate_up, x, a, b, scale, base, out, plan}, false, stream));
+  MOE_CUDA_TRY(launch_adapter_apply(s, AdapterApply{gate_up, x, a, b, scale, base, out, plan, static_cast<int*>(plan),
+                                                   wait_limit(cfg)}, false, stream));
   return MOE_OK;
 }
 
@@ -339,12 +340,12 @@ cudaError_t run_adapted_ffn(const moe_config* c, const Carve& k, const moe_adapt
               a1 ? kFfnGemm1Plain : kFfnGemm1);
   if (e != cudaSuccess) return e;
   if (a1) {
-    e = launch_adapter_apply(sh, AdapterApply{true, x, a1, b1, ad->scale, pre, h, plan}, true, s);
+    e = launch_adapter_apply(sh, AdapterApply{true, x, a1, b1, ad->scale, pre, h, plan, k.status, wait_limit(c)}, true, s);
     if (e != cudaSuccess) return e;
   }
   e = run_ffn(c, k, x, offsets, G, rows, f, w_gu, w_d, h, y, s, shared, true, true, kFfnGemm2);
   if (e != cudaSuccess || !a2) return e;
-  return launch_adapter_apply(sh, AdapterApply{false, h, a2, b2, ad->scale, y, y, plan}, true, s);
+  return launch_adapter_apply(sh, AdapterApply{false, h, a2, b2, ad->scale, y, y, plan, k.status, wait_limit(c)}, true, s);
 }
 
 }  // namespace
