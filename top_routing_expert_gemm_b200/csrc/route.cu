@@ -25,10 +25,12 @@
 // the warp decides the row again in binary64.  Measured on N(0, 1) logits with
 // 256 experts: well under one row in a hundred.
 //
-// One warp per row: lane L holds the NC consecutive columns from L * NC, so a
-// lower lane is a lower index, ties resolve by the lowest set bit of a ballot,
-// and an aligned group is a run of lanes.  A pick is one redux.sync maximum of
-// order-preserving integer keys and one ballot.
+// One warp per row: lane L holds the NC consecutive columns from L * NC, so an
+// aligned group is a run of lanes.  Choices are compared as order-preserving
+// integers, the picks come from a few candidates (pick_candidates).  Measured (8192 x 256, sigmoid, 8 groups, k = 8): RANK_US us,
+// against 33 us for k rounds of maximum, owner and removal; 65536 x 128 in bf16
+// with k = 4: RANK2_US against 61 us.  (A thread per row over a tile in shared
+// memory, two-level maxima per thread: 75 and 39 us.)
 #include <type_traits>
 
 #include "common.cuh"
@@ -56,13 +58,24 @@ __device__ __forceinline__ float usable(float l) {
   return l > lowest<T>() ? fminf(l, 3.40282346638528859812e38f) : -INFINITY;
 }
 
-// order-preserving integer of a float; 0 only for what must not be picked
+// Order-preserving integer of a float: 0 for -inf and NaN (what must not be
+// picked), -0 and +0 alike.
 __device__ __forceinline__ uint32_t key_of(float f) {
-  const uint32_t b = __float_as_uint(f + 0.0f);  // -0 and +0 are one key
-  return f > -INFINITY ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
+  const int b = __float_as_int(f + 0.0f);
+  return f > -INFINITY ? (uint32_t)(b ^ (b >> 31 | (int)0x80000000)) : 0u;
 }
 __device__ __forceinline__ float float_of(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// 1 / (1 + e^-l) for the comparisons: the hardware's exponential (2^-22, and
+// 2^-24 |l| from its argument, both weighted with s (1 - s)), one rounded sum
+// and the hardware's reciprocal (2^-23) leave less than 2^-21.8.
+__device__ __forceinline__ float sigmoid_fast(float l) {
+  float e, q;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
+  return q;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -206,9 +219,72 @@ __device__ __noinline__ int pick_any(F (&c)[NC], const RouteArgs& p, int lane, F
   return id;
 }
 
+// The k largest of the warp's columns from a few candidates.  key orders the
+// columns as val does or more coarsely (equal keys of different values), 0 is
+// not to be picked.  The k + 1 largest lane maxima give a threshold that at
+// least k + 1 columns reach and hardly more; those are gathered in shared
+// memory, one per lane, and each counts the candidates before it (larger val,
+// or equal and a lower column): its rank.  Returns the number of candidates, over
+// 32 if ties leave too many (then nothing else is done); lane s holds the
+// candidate of rank s.
+template <typename V>
+struct Picks {
+  V val[32];
+  int col[32];
+};
+template <typename V, int NC>
+__device__ __forceinline__ int pick_candidates(const uint32_t (&key)[NC], const V (&val)[NC], int k, int c0, int lane,
+                                               Picks<V>* cand, Picks<V>* order) {
+  uint32_t left = key[0], tau = 0;
+#pragma unroll
+  for (int j = 1; j < NC; ++j) left = max(left, key[j]);
+  for (int s = 0; s <= k; ++s) {
+    tau = __reduce_max_sync(kFull, left);
+    if (left == tau) left = 0;  // lanes that tie leave together: tau only falls lower
+  }
+  tau = max(tau, 1u);
+  int mine = 0;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) mine += key[j] >= tau;
+  int at = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(kFull, at, off);
+    if (lane >= off) at += o;
+  }
+  const int n = __shfl_sync(kFull, at, 31);
+  if (n > 32) return n;
+  at -= mine;
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+    if (key[j] >= tau) {
+      cand->val[at] = val[j];
+      cand->col[at] = c0 + j;
+      ++at;
+    }
+  __syncwarp();
+  const V v = lane < n ? cand->val[lane] : V(0);
+  const int c = lane < n ? cand->col[lane] : 0;
+  int rank = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const V o = cand->val[i];
+    // the candidates of a lane, and the lanes, come in ascending columns
+    rank += o > v || (o == v && i < lane);
+  }
+  if (lane < n) {
+    order->val[rank] = v;
+    order->col[rank] = c;
+  }
+  __syncwarp();
+  return n;
+}
+
 // The row again in binary64: scores from the fp32 or bf16 logits as stored.
+// runs: groups are aligned runs of lanes_g lanes.
 template <typename T, int NC>
-__device__ __noinline__ int pick_exact(const RouteArgs& p, const T* row, int lane) {
+__device__ __noinline__ int pick_exact(const RouteArgs& p, const T* row, int lane, bool runs, int lanes_g,
+                                       Picks<double>* cand, Picks<double>* order) {
   const int c0 = lane * NC;
   double c[NC];
   double m = -(double)INFINITY;
@@ -227,14 +303,48 @@ __device__ __noinline__ int pick_exact(const RouteArgs& p, const T* row, int lan
     z = warp_sum(z);
   }
 #pragma unroll
-  for (int j = 0; j < NC; ++j)
-    if (c[j] > -(double)INFINITY) {
-      const double s = p.sigmoid ? 1.0 / (1.0 + exp(-c[j])) : exp(c[j] - m) / z;
-      const double v = s + (p.bias ? (double)p.bias[c0 + j] : 0.0);
-      c[j] = v == v ? v : -(double)INFINITY;
+  for (int j = 0; j < NC; ++j) {
+    const double s = p.sigmoid ? 1.0 / (1.0 + exp(-c[j])) : exp(c[j] - m) / z;
+    const double v = s + (p.bias && c0 + j < p.E ? (double)p.bias[c0 + j] : 0.0);
+    c[j] = c[j] > -(double)INFINITY && v == v ? v : -(double)INFINITY;
+  }
+  if (p.G == 1 || runs) {
+    bool kept = true;
+    if (p.G > 1) {
+      double a = -(double)INFINITY, b = a;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        b = fmax(b, fmin(a, c[j]));
+        a = fmax(a, c[j]);
+      }
+      for (int off = 1; off < lanes_g; off <<= 1) {
+        const double oa = __shfl_xor_sync(kFull, a, off), ob = __shfl_xor_sync(kFull, b, off);
+        b = fmax(fmin(a, oa), fmax(b, ob));
+        a = fmax(a, oa);
+      }
+      if (p.group_top == 2 && b > -(double)INFINITY) a += b;
+      int rank = 0;
+      for (int g = 0; g < p.G; ++g) {
+        const double o = __shfl_sync(kFull, a, g * lanes_g);
+        rank += o > a || (o == a && g < lane / lanes_g);
+      }
+      kept = c0 < p.E && rank < p.Gk;
     }
+    uint32_t key[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) key[j] = kept ? key_of(fmaxf((float)c[j], c[j] > -(double)INFINITY ? lowest<float>() : -INFINITY)) : 0u;
+    const int n = pick_candidates<double, NC>(key, c, p.k, c0, lane, cand, order);
+    if (n <= 32) {
+      const int id = lane < min(n, p.k) ? order->col[lane] : -1;
+      __syncwarp();
+      return id;
+    }
+  }
+  double v[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) v[j] = c[j];
   bool unused;
-  return pick_any<double, NC>(c, p, lane, 0.0, &unused);
+  return pick_any<double, NC>(v, p, lane, 0.0, &unused);
 }
 
 // lanes < k of the warp hold a picked expert's logit l (-inf: empty slot):
@@ -255,6 +365,10 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
   const int lane = threadIdx.x % 32;
   const int c0 = lane * NC;
   const T* __restrict__ logits = static_cast<const T*>(p.logits);
+  __shared__ Picks<double> s_picks[kWarps][2];  // candidates, and in order (also as floats)
+  Picks<double>* exact = s_picks[threadIdx.x / 32];
+  Picks<float>* cand = reinterpret_cast<Picks<float>*>(&exact[0]);
+  Picks<float>* order = reinterpret_cast<Picks<float>*>(&exact[1]);
   const int64_t step = (int64_t)gridDim.x * kWarps;
   int64_t t = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
   if (threadIdx.x == 0) grid_launch_dependents();  // the dispatch may be scheduled (it waits for these ids)
@@ -270,10 +384,11 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
     if (b[j] > -INFINITY) bmax = fmaxf(bmax, fabsf(b[j]));
   }
   bmax = warp_max(bmax);
-  // groups as aligned runs of lanes: a power-of-two number of whole lanes each
+  // groups as aligned runs of lanes, a power-of-two number of whole lanes each
   const int gs = p.E / p.G;
   const int lanes_g = gs / NC;
   const bool runs = p.G > 1 && gs % NC == 0 && (lanes_g & (lanes_g - 1)) == 0;
+  // (otherwise pick_any decides)
   // c is increasing in l (no bias or a zero one, no sum over a group's two
   // best): compare logits
   bool zero = true;
@@ -294,8 +409,8 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
     if (t + step < p.T) load_cols<T, NC>(row + step * p.stride, c0, p.E, p.vec, next);
 
     // ---- choices and the bound on the error of a difference of two of them.
-    // sigmoid: s is off by less than 2^-21 (__expf and __fdividef at their
-    // documented bounds), the sum with b by 2^-24 (1 + |b|).  softmax: every
+    // sigmoid: s is off by less than 2^-21 (sigmoid_fast), the sum with b by
+    // 2^-24 (1 + |b|).  softmax: every
     // probability is off by less than 2^-18 of the largest (the terms'
     // errors and the up to 37 additions of the denominator).
     float eps = 0.f, z = 1.f;
@@ -310,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
       if (p.sigmoid) {
 #pragma unroll
         for (int j = 0; j < NC; ++j)
-          if (c[j] > -INFINITY) c[j] = __fdividef(1.0f, 1.0f + __expf(-c[j])) + b[j];
+          c[j] = c[j] > -INFINITY ? sigmoid_fast(c[j]) + b[j] : -INFINITY;
         eps = 0x1p-19f * (1.0f + bmax);
       } else {
         const float inv = 1.0f / z;
@@ -322,12 +437,13 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
     }
 
     int id = -1;
+    float l = -INFINITY;  // lane s < k: the logit of slot s
     bool near = false;
     if (p.G > 1 && !runs) {
+      float v[NC];  // pick_any takes its values by address: c stays in registers
 #pragma unroll
-      for (int j = 0; j < NC; ++j)
-        if (!(c[j] == c[j])) c[j] = -INFINITY;  // a NaN bias masks too
-      id = pick_any<float, NC>(c, p, lane, eps, &near);
+      for (int j = 0; j < NC; ++j) v[j] = c[j] == c[j] ? c[j] : -INFINITY;  // a NaN bias masks too
+      id = pick_any<float, NC>(v, p, lane, eps, &near);
     } else {
       uint32_t key[NC];
 #pragma unroll
@@ -363,40 +479,53 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
           for (int j = 0; j < NC; ++j) key[j] = 0;
         }
       }
-      // ---- k picks: the largest key of the warp, the lowest lane that holds it
-      uint32_t best = key[0];
-#pragma unroll
-      for (int j = 1; j < NC; ++j) best = max(best, key[j]);
-      float prev = INFINITY;
-      for (int s = 0; s < p.k; ++s) {
-        const uint32_t top = __reduce_max_sync(kFull, best);
-        if (top == 0) break;
-        const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
-        int at = 0;
-        if (lane == owner) {
-#pragma unroll
-          for (int j = NC - 1; j >= 0; --j) at = key[j] == top ? j : at;
-          best = 0;
-#pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            key[j] = j == at ? 0u : key[j];
-            best = max(best, key[j]);
-          }
-          at += c0;
+      const int n = pick_candidates<float, NC>(key, c, p.k, c0, lane, cand, order);
+      if (n <= 32) {
+        if (lane < min(n, p.k)) {
+          id = order->col[lane];
+          l = order->val[lane];
+          near |= lane + 1 < n && l - order->val[lane + 1] < eps;
         }
-        at = __shfl_sync(kFull, at, owner);
-        if (lane == s) id = at;
-        const float v = float_of(top);
-        near |= prev - v < eps;
-        prev = v;
+        near = __any_sync(kFull, near);
+      } else {
+        // more columns tie than a warp has lanes: k rounds of the largest key,
+        // the lowest lane that holds it, and its lowest column
+        uint32_t best = key[0];
+#pragma unroll
+        for (int j = 1; j < NC; ++j) best = max(best, key[j]);
+        float prev = INFINITY;
+        for (int s = 0; s <= p.k; ++s) {  // the round after the last only looks how close the next one was
+          const uint32_t top = __reduce_max_sync(kFull, best);
+          if (top == 0) break;
+          const float v = float_of(top);
+          near |= prev - v < eps;
+          prev = v;
+          const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
+          int at = 0;
+          if (lane == owner) {
+#pragma unroll
+            for (int j = NC - 1; j >= 0; --j) at = key[j] == top ? j : at;
+            best = 0;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+              key[j] = j == at ? 0u : key[j];
+              best = max(best, key[j]);
+            }
+            at += c0;
+          }
+          at = __shfl_sync(kFull, at, owner);
+          if (lane == s && s < p.k) {
+            id = at;
+            l = v;
+          }
+        }
       }
-      const uint32_t rest = __reduce_max_sync(kFull, best);
-      near |= rest && prev - float_of(rest) < eps;
+      __syncwarp();  // the candidates are read before the next row's are written
     }
-    if (near) id = pick_exact<T, NC>(p, row, lane);
+    if (near) id = pick_exact<T, NC>(p, row, lane, runs, lanes_g, &exact[0], &exact[1]);
 
-    // ---- weights: lane s < k holds slot s
-    const float l = id >= 0 ? usable<T>(Elem<T>::to_f(row[id])) : -INFINITY;
+    // ---- weights: lane s < k holds slot s (its choice is its logit, or the row is read again)
+    if (!by_logit || (p.G > 1 && !runs)) l = id >= 0 ? usable<T>(Elem<T>::to_f(row[id])) : -INFINITY;
     const float top = p.renorm ? warp_max(l) : 0.f;
     float zw = z;
     if (!p.sigmoid && !p.renorm) {  // probabilities as they are: the denominator with expf
