@@ -111,7 +111,7 @@ def test_route_batch_sizes(T):
     assert torch.equal(ids, again) and torch.equal(w, w2)
 
 
-def _repeated(l, T=1061):
+def _repeated(l, T=8219):
     """The rows of l over and over, in the same padded layout."""
     wide = torch.full((T, l.stride(0)), 99.0, device="cuda").to(l.dtype)
     wide[:, :l.shape[1]] = l.repeat(-(-T // l.shape[0]), 1)[:T]
@@ -123,15 +123,15 @@ def _repeated(l, T=1061):
 @pytest.mark.parametrize("dtype,bias,masks,pad", [("f32", True, 0.0, 0), ("bf16", False, 0.3, 3),
                                                   ("f32", False, 0.1, 8), ("bf16", True, 0.7, 0)])
 def test_route_of_many_rows_matches_the_oracle(score, E, k, G, Gk, gtop, dtype, bias, masks, pad):
-    """Batches large enough for a thread per row, on the rows of the test above."""
+    """Batches large enough for four threads per row, on the rows of the test above."""
     few = _logits(53, E, dtype, E + k, masks, pad)
     l = _repeated(few)
     b = (0.2 * torch.randn(E, generator=torch.Generator().manual_seed(1))).cuda() if bias else None
     for renorm, scale in ((1, 2.5), (0, 1.0)):
         cfg = _cfg(l, k, score, G, Gk, gtop, renorm, scale)
         ids, w = _run(l, b, cfg)
-        assert torch.equal(ids[53:106], ids[:53]) and torch.equal(ids[1007:1060], ids[:53])
-        assert torch.equal(w[53:106], w[:53]) and torch.equal(w[1060], w[0])
+        assert torch.equal(ids[53:106], ids[:53]) and torch.equal(ids[8162:8215], ids[:53])
+        assert torch.equal(w[53:106], w[:53]) and torch.equal(w[8215], w[0])
         _check(few, b, _cfg(few, k, score, G, Gk, gtop, renorm, scale), score, ids[:53], w[:53], dtype)
 
 
@@ -155,7 +155,7 @@ def test_choices_closer_than_fp32_are_decided_as_the_logits_say(score, G, Gk, gt
     many = _repeated(lt)
     ids2, w2 = _run(many, bias, _cfg(many, k, score, G, Gk, gtop))
     _check(lt, bias, cfg, score, ids2[:T], w2[:T], "f32")
-    assert torch.equal(ids2[-37:], ids2[1061 - 37 - T:1061 - T])
+    assert torch.equal(ids2[-37:], ids2[8219 - 37 - T:8219 - T])
 
 
 def test_ties_zero_bias_and_equal_rows_take_the_lowest_index():
@@ -170,7 +170,7 @@ def test_ties_zero_bias_and_equal_rows_take_the_lowest_index():
                 _check(l, bias, cfg, score, ids, w, "f32")
                 many = _repeated(l)
                 ids2, _ = _run(many, bias, _cfg(many, 3, score, G, Gk, gtop))
-                assert torch.equal(ids2[9:18], ids) and torch.equal(ids2[1035:1044], ids)
+                assert torch.equal(ids2[9:18], ids) and torch.equal(ids2[8208:8217], ids)
 
 
 def test_extreme_logits_and_biases():

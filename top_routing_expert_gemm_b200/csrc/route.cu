@@ -22,15 +22,13 @@
 // and the logits themselves are compared: exact.  Otherwise a row is decided
 // in fp32 with a bound on its error, and where two neighbours in the order
 // (or the last kept and the first dropped group) are closer than the bound,
-// the warp decides the row again in binary64.  Measured on N(0, 1) logits with
-// 256 experts: well under one row in a hundred.
+// the warp decides it again in binary64, as a rule over the few columns within
+// reach (pick_near): about one row in three thousand of N(0, 1) logits, 256
+// experts and a bias, and some 5 us for a warp that meets one.
 //
 // One warp per row: lane L holds the NC consecutive columns from L * NC, so an
 // aligned group is a run of lanes.  Choices are compared as order-preserving
-// integers, the picks come from a few candidates (pick_candidates).  Measured (8192 x 256, sigmoid, 8 groups, k = 8): RANK_US us,
-// against 33 us for k rounds of maximum, owner and removal; 65536 x 128 in bf16
-// with k = 4: RANK2_US against 61 us.  (A thread per row over a tile in shared
-// memory, two-level maxima per thread: 75 and 39 us.)
+// integers, the picks come from a few candidates (pick_candidates).
 #include <type_traits>
 
 #include "common.cuh"
@@ -70,7 +68,7 @@ __device__ __forceinline__ float float_of(uint32_t k) {
 
 // 1 / (1 + e^-l) for the comparisons: the hardware's exponential (2^-22, and
 // 2^-24 |l| from its argument, both weighted with s (1 - s)), one rounded sum
-// and the hardware's reciprocal (2^-23) leave less than 2^-21.8.
+// (2^-24 s) and the hardware's reciprocal (2^-23 s) leave less than 1.65 2^-23.
 __device__ __forceinline__ float sigmoid_fast(float l) {
   float e, q;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
@@ -79,9 +77,23 @@ __device__ __forceinline__ float sigmoid_fast(float l) {
 }
 
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+  asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
   return v;
+}
+// e^x to about 2^-21.5 of its value for any x (0 below 2^-126): the hardware's 2^t (2^-22) of the
+// rounded t = x log2 e, corrected by what the rounding left out
+__device__ __forceinline__ float exp_near(float x) {
+  const float t = x * 1.4426950408889634f;
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  const float left = fmaf(x, 1.4426950408889634f, -t);
+  return fabsf(x) < 100.0f ? fmaf(e, left * 0.6931471805599453f, e) : e;  // beyond, e is 0 or infinite
+}
+// 1 / x to 2^-23 (x of ordinary size, or infinite: 0)
+__device__ __forceinline__ float rcp_near(float x) {
+  float q;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(x));
+  return q;
 }
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
@@ -347,6 +359,52 @@ __device__ __noinline__ int pick_exact(const RouteArgs& p, const T* row, int lan
   return pick_any<double, NC>(v, p, lane, 0.0, &unused);
 }
 
+// The picks of a row whose kept groups are certain but whose order is not: only
+// the columns within reach of the k-th best, vk, can be picked, so only those
+// (one per lane, seldom more than k + 2) are computed in binary64.  thr: vk less
+// the bound; m, inv: the softmax's maximum and 1 / denominator.  Returns the
+// number of candidates; over 32, nothing is decided.  Not unrolled: it runs for
+// one row in a thousand, and its instructions come from far away.
+template <typename T>
+__device__ __noinline__ int pick_near(const RouteArgs& p, const T* row, int lane, uint32_t kept, float thr, float m,
+                                      float inv, Picks<double>* cand, int* id) {
+  const int gs = p.E / p.G;
+  int n = 0;
+  double z = 0.0;
+#pragma unroll 1
+  for (int c0 = 0; c0 < p.E; c0 += 32) {
+    const int c = c0 + lane;
+    const float l = c < p.E ? usable<T>(Elem<T>::to_f(row[c])) : -INFINITY;
+    if (!p.sigmoid && l > -INFINITY) z += exp((double)l - (double)m);
+    const float v = (p.sigmoid ? sigmoid_fast(l) : __expf(l - m) * inv) + (p.bias && c < p.E ? p.bias[c] : 0.f);
+    const bool in = l > -INFINITY && v >= thr && (p.G == 1 || kept >> (c / gs) & 1u);
+    const unsigned who = __ballot_sync(kFull, in);
+    const int at = n + __popc(who & ((1u << lane) - 1u));
+    if (in && at < 32) cand->col[at] = c;
+    n += __popc(who);
+  }
+  if (n > 32) return n;
+  z = warp_sum(z);
+  __syncwarp();
+  const int c = lane < n ? cand->col[lane] : 0;
+  const double l = (double)usable<T>(Elem<T>::to_f(row[c]));
+  const double num = p.sigmoid ? 1.0 : exp(l - (double)m);
+  const double v = num / (p.sigmoid ? 1.0 + exp(-l) : z) + (p.bias ? (double)p.bias[c] : 0.0);
+  cand->val[lane] = v;
+  __syncwarp();
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const double o = cand->val[i];
+    rank += o > v || (o == v && i < lane);
+  }
+  __syncwarp();
+  if (lane < n) cand->col[rank] = c;
+  __syncwarp();
+  *id = lane < min(n, p.k) ? cand->col[lane] : -1;
+  __syncwarp();
+  return n;
+}
+
 // lanes < k of the warp hold a picked expert's logit l (-inf: empty slot):
 // the weight before scaling and renormalisation, relative to a factor shared
 // by the row's picks (which the renormalisation divides out): sigmoid scores
@@ -354,14 +412,14 @@ __device__ __noinline__ int pick_exact(const RouteArgs& p, const T* row, int lan
 __device__ __forceinline__ float picked_score(bool sigmoid, bool renorm, float l, float top, float m, float z) {
   if (!(l > -INFINITY)) return 0.f;
   if (sigmoid) {
-    if (renorm && top < 0.f) return expf(l - top) / (1.0f + expf(l));
-    return 1.0f / (1.0f + expf(-l));
+    if (renorm && top < 0.f) return exp_near(l - top) * rcp_near(1.0f + exp_near(l));
+    return rcp_near(1.0f + exp_near(-l));
   }
-  return renorm ? expf(l - top) : expf(l - m) / z;
+  return renorm ? exp_near(l - top) : exp_near(l - m) * rcp_near(z);
 }
 
 template <typename T, int NC>
-__global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p) {
+__global__ void __launch_bounds__(kThreads) route_topk_kernel(const __grid_constant__ RouteArgs p) {
   const int lane = threadIdx.x % 32;
   const int c0 = lane * NC;
   const T* __restrict__ logits = static_cast<const T*>(p.logits);
@@ -408,9 +466,11 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
     }
     if (t + step < p.T) load_cols<T, NC>(row + step * p.stride, c0, p.E, p.vec, next);
 
-    // ---- choices and the bound on the error of a difference of two of them.
-    // sigmoid: s is off by less than 2^-21 (sigmoid_fast), the sum with b by
-    // 2^-24 (1 + |b|).  softmax: every
+    // ---- choices and eps, the bound on the error of a difference of two of them
+    // (of two group scores: 2 eps).  sigmoid: s is off by less than 1.65 2^-23
+    // (sigmoid_fast), the sum with b by 2^-24 (1 + |b|), so a difference of two
+    // by less than 2^-22 (2.15 + 0.5 |b|); a sum of two adds its own rounding,
+    // 2^-23 (1 + |b|): 2^-22 (5.3 + 2 |b|) for a difference of group scores.  softmax: every
     // probability is off by less than 2^-18 of the largest (the terms'
     // errors and the up to 37 additions of the denominator).
     float eps = 0.f, z = 1.f;
@@ -426,7 +486,7 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
 #pragma unroll
         for (int j = 0; j < NC; ++j)
           c[j] = c[j] > -INFINITY ? sigmoid_fast(c[j]) + b[j] : -INFINITY;
-        eps = 0x1p-19f * (1.0f + bmax);
+        eps = 0x1p-22f * (2.75f + bmax);
       } else {
         const float inv = 1.0f / z;
 #pragma unroll
@@ -438,12 +498,14 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
 
     int id = -1;
     float l = -INFINITY;  // lane s < k: the logit of slot s
-    bool near = false;
+    bool near = false, near_group = false;
+    uint32_t groups = 0xffffffffu;  // the kept ones
+    float vk = INFINITY;            // the last pick's choice
     if (p.G > 1 && !runs) {
       float v[NC];  // pick_any takes its values by address: c stays in registers
 #pragma unroll
       for (int j = 0; j < NC; ++j) v[j] = c[j] == c[j] ? c[j] : -INFINITY;  // a NaN bias masks too
-      id = pick_any<float, NC>(v, p, lane, eps, &near);
+      id = pick_any<float, NC>(v, p, lane, eps, &near_group);  // which of the two was close is not told
     } else {
       uint32_t key[NC];
 #pragma unroll
@@ -473,7 +535,8 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
         const bool kept = c0 < p.E && rank < p.Gk;
         const uint32_t lo = __reduce_min_sync(kFull, kept ? gk : 0xffffffffu);
         const uint32_t hi = __reduce_max_sync(kFull, kept ? 0u : gk);
-        near = hi && float_of(lo) - float_of(hi) < 2.0f * eps;
+        near_group = hi && float_of(lo) - float_of(hi) < 2.0f * eps;
+        groups = __reduce_or_sync(kFull, kept ? 1u << mine : 0u);
         if (!kept) {
 #pragma unroll
           for (int j = 0; j < NC; ++j) key[j] = 0;
@@ -487,6 +550,7 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
           near |= lane + 1 < n && l - order->val[lane + 1] < eps;
         }
         near = __any_sync(kFull, near);
+        vk = n > 0 ? order->val[min(n, p.k) - 1] : INFINITY;
       } else {
         // more columns tie than a warp has lanes: k rounds of the largest key,
         // the lowest lane that holds it, and its lowest column
@@ -500,6 +564,7 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
           const float v = float_of(top);
           near |= prev - v < eps;
           prev = v;
+          vk = s < p.k ? v : vk;
           const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
           int at = 0;
           if (lane == owner) {
@@ -522,7 +587,9 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
       }
       __syncwarp();  // the candidates are read before the next row's are written
     }
-    if (near) id = pick_exact<T, NC>(p, row, lane, runs, lanes_g, &exact[0], &exact[1]);
+    if (near && !near_group && pick_near<T>(p, row, lane, groups, vk - eps, m, 1.0f / z, &exact[0], &id) > 32)
+      near_group = true;
+    if (near_group) id = pick_exact<T, NC>(p, row, lane, runs, lanes_g, &exact[0], &exact[1]);
 
     // ---- weights: lane s < k holds slot s (its choice is its logit, or the row is read again)
     if (!by_logit || (p.G > 1 && !runs)) l = id >= 0 ? usable<T>(Elem<T>::to_f(row[id])) : -INFINITY;
@@ -535,7 +602,7 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const float lu = usable<T>(lr[j]);
-        zw += lu > -INFINITY ? expf(lu - m) : 0.f;
+        zw += lu > -INFINITY ? exp_near(lu - m) : 0.f;
       }
       zw = warp_sum(zw);
     }
@@ -547,6 +614,337 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
     if (lane < p.k) {
       p.ids[t * p.k + lane] = id;
       p.w[t * p.k + lane] = w * p.scale;
+    }
+  }
+}
+
+// Four threads per row, 32 rows per block, so that every instruction serves 8
+// rows.  A row's columns are cut into blocks of up to 16 inside its groups;
+// thread q takes the blocks q, q + 4, ...: it loads them (16-byte loads where rows
+// and blocks are aligned), computes their choices, leaves them in shared memory
+// and keeps the block maxima in registers.  A pick is the maximum of the block
+// maxima (the first of equals) over the four threads; together they search that
+// block for the column and for what its maximum is without it.
+constexpr int kTileRows = 32;
+
+struct TileShape {
+  int gs, nbg, bl, blp, nb;  // columns of a group, blocks of it, columns of a block and their pitch, blocks
+  int pitch, bmp;            // floats per row of the choices, and of the block maxima
+};
+__host__ __device__ inline TileShape tile_shape(int E, int G) {
+  TileShape s;
+  s.gs = E / G;
+  s.nbg = (s.gs + 15) / 16;
+  s.bl = (s.gs + 4 * s.nbg - 1) / (4 * s.nbg) * 4;
+  s.blp = s.bl + 4;
+  s.nb = G * s.nbg;
+  // rows 16 floats apart modulo 32 and blocks 20: the four threads' 16-byte writes of two rows meet no bank conflict
+  s.pitch = (s.nb * s.blp + 15) / 32 * 32 + 16;
+  if (s.pitch < s.nb * s.blp) s.pitch += 32;
+  s.bmp = s.nb | 1;
+  return s;
+}
+__host__ __device__ inline size_t tile_smem(int E, int G) {
+  const TileShape s = tile_shape(E, G);
+  return sizeof(float) * (kTileRows * (size_t)(s.pitch + (G > 1 ? 2 * s.bmp + G : 0) + kMaxTopK) + 16 * s.nb) +
+         kWarps * 2 * sizeof(Picks<double>);
+}
+// blocks of a row per thread, for E <= 32 NC
+template <int NC>
+constexpr int kTileBlocks = NC <= 4 ? 2 : NC / 2;
+
+// n <= 16 columns as stored, -inf behind them (vec: in 16-byte loads)
+template <typename T>
+__device__ __forceinline__ void load_block(const T* row, int n, bool vec, float (&v)[16]) {
+  constexpr int V = 16 / sizeof(T);
+  if (vec) {  // n is a multiple of V
+#pragma unroll
+    for (int i = 0; i < 16 / V; ++i) {
+      Vec16<T> x;
+      if (i * V < n) x = ld16(row + i * V);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[i * V + e] = i * V < n ? Elem<T>::to_f(x.v[e]) : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = j < n ? Elem<T>::to_f(row[j]) : -INFINITY;
+  }
+}
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
+  return fmaxf(v, __shfl_xor_sync(kFull, v, 2));
+}
+
+template <typename T, int NC>
+__global__ void __launch_bounds__(kThreads) route_tile_kernel(const __grid_constant__ RouteArgs p) {
+  constexpr int NB = kTileBlocks<NC>;
+  extern __shared__ __align__(16) float sm[];
+  const TileShape sh = tile_shape(p.E, p.G);
+  const int lane = threadIdx.x % 32, r = threadIdx.x / 4, q = threadIdx.x % 4;
+  float* row_c = sm + r * sh.pitch;                                      // the row's choices, block after block
+  float* s_bias = sm + kTileRows * sh.pitch;                             // [nb][16] bias, 0 behind a block
+  float* row_id = s_bias + 16 * sh.nb + r * kMaxTopK;                    // the row's picks
+  float* grp = s_bias + 16 * sh.nb + kTileRows * kMaxTopK;               // G > 1:
+  float* bm = grp + r * (2 * sh.bmp + p.G);                              //   block maxima,
+  float* bm2 = bm + sh.bmp;                                              //   and seconds,
+  float* score = bm2 + sh.bmp;                                           //   group scores
+  const size_t head = tile_smem(p.E, p.G) - kWarps * 2 * sizeof(Picks<double>);
+  Picks<double>* exact = reinterpret_cast<Picks<double>*>(reinterpret_cast<uint8_t*>(sm) + head) + threadIdx.x / 32 * 2;
+  if (threadIdx.x == 0) grid_launch_dependents();  // the dispatch may be scheduled (it waits for these ids)
+  const int64_t t = (int64_t)blockIdx.x * kTileRows + r;
+  const bool live = t < p.T;
+  const T* row = static_cast<const T*>(p.logits) + (live ? t : 0) * p.stride;
+
+  // ---- the bias: in shared memory, zero throughout?, and its largest
+  float bmax = 0.f;
+  bool zero = true;
+  if (p.bias) {
+    for (int i = threadIdx.x; i < 16 * sh.nb; i += kThreads) {
+      const int b = i / 16, j = i % 16, at = b % sh.nbg * sh.bl + j;
+      const float v = j < sh.bl && at < sh.gs ? p.bias[b / sh.nbg * sh.gs + at] : 0.f;
+      s_bias[i] = v == v ? v : -INFINITY;  // a NaN bias masks too
+      if (v > -INFINITY) bmax = fmaxf(bmax, fabsf(v));
+      zero &= v == 0.f;
+    }
+    zero = __syncthreads_and(zero);
+  }
+  const bool by_logit = zero && (p.G == 1 || p.group_top == 1);
+  const bool need_z = !p.sigmoid && (!by_logit || !p.renorm);
+  if (!zero) {
+    bmax = warp_max(bmax);
+    float* part = reinterpret_cast<float*>(exact - threadIdx.x / 32 * 2);
+    if (lane == 0) part[threadIdx.x / 32] = bmax;
+    __syncthreads();
+    bmax = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    __syncthreads();
+  }
+  // whole vectors: rows on 16 bytes, groups and blocks of whole vectors
+  const bool vec = p.vec && sh.gs * sizeof(T) % 16 == 0 && sh.bl * sizeof(T) % 16 == 0;
+
+  float m = -INFINITY, z = 0.f, inv = 1.f;
+  if (need_z) {
+    for (int b = q; b < sh.nb; b += 4) {
+      const int at = b % sh.nbg * sh.bl;
+      float v[16];
+      load_block<T>(row + b / sh.nbg * sh.gs + at, min(sh.bl, sh.gs - at), vec, v);
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        v[j] = usable<T>(v[j]);
+        top = fmaxf(top, v[j]);
+      }
+      if (top > m) {
+        z *= exp_near(m - top);
+        m = top;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) z += v[j] > -INFINITY ? exp_near(v[j] - m) : 0.f;
+    }
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      const float om = __shfl_xor_sync(kFull, m, off), oz = __shfl_xor_sync(kFull, z, off);
+      const float top = fmaxf(m, om);
+      z = (m > -INFINITY ? z * exp_near(m - top) : 0.f) + (om > -INFINITY ? oz * exp_near(om - top) : 0.f);
+      m = top;
+    }
+    inv = 1.0f / z;
+  }
+  // the bounds of route_topk_kernel
+  const float eps = by_logit    ? 0.f
+                    : p.sigmoid ? 0x1p-22f * (2.75f + bmax)
+                                : 0x1p-17f * inv + 0x1p-22f * (bmax + 1.0f * inv);
+
+  // ---- choices and block maxima; four blocks are loaded at a time
+  const bool seconds = p.G > 1 && p.group_top == 2;
+  float top[NB];
+  constexpr int NL = NB < 4 ? NB : 4;
+#pragma unroll
+  for (int i0 = 0; i0 < NB; i0 += NL) {
+    float v[NL][16];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int b = q + 4 * (i0 + i), at = b % sh.nbg * sh.bl;
+      load_block<T>(row + b / sh.nbg * sh.gs + at, live && b < sh.nb ? min(sh.bl, sh.gs - at) : 0, vec, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int b = q + 4 * (i0 + i);
+      float best = -INFINITY;
+      if (b < sh.nb) {
+        if (by_logit) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[i][j] = usable<T>(v[i][j]);
+        } else {
+          float add[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 f = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(s_bias + 16 * b)[j];
+            add[4 * j] = f.x;
+            add[4 * j + 1] = f.y;
+            add[4 * j + 2] = f.z;
+            add[4 * j + 3] = f.w;
+          }
+          if (p.sigmoid) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[i][j] = v[i][j] > lowest<T>() ? sigmoid_fast(v[i][j]) + add[j] : -INFINITY;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              v[i][j] = v[i][j] > lowest<T>() ? fmaf(__expf(usable<T>(v[i][j]) - m), inv, add[j]) : -INFINITY;
+          }
+        }
+        float second = -INFINITY;
+        if (seconds) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            second = fmaxf(second, fminf(best, v[i][j]));
+            best = fmaxf(best, v[i][j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) best = fmaxf(best, v[i][j]);
+        }
+        float4* dst = reinterpret_cast<float4*>(row_c + b * sh.blp);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (4 * j < sh.bl) dst[j] = make_float4(v[i][4 * j], v[i][4 * j + 1], v[i][4 * j + 2], v[i][4 * j + 3]);
+        if (p.G > 1) {
+          bm[b] = best;
+          bm2[b] = second;
+        }
+      }
+      top[i0 + i] = best;
+    }
+  }
+  __syncwarp();
+
+  bool near = false, near_group = false;
+  uint32_t kept = 0xffffffffu;  // groups
+  if (p.G > 1) {  // thread q scores and ranks the groups q, q + 4, ...
+    for (int g = q; g < p.G; g += 4) {
+      float a = -INFINITY, a2 = -INFINITY;
+      for (int i = g * sh.nbg; i < (g + 1) * sh.nbg; ++i) {
+        a2 = fmaxf(fminf(a, bm[i]), fmaxf(a2, bm2[i]));
+        a = fmaxf(a, bm[i]);
+      }
+      score[g] = p.group_top == 2 && a2 > -INFINITY ? a + a2 : a;
+    }
+    __syncwarp();
+    kept = 0;
+    float lo = INFINITY, hi = -INFINITY;
+    for (int g = q; g < p.G; g += 4) {
+      const float v = score[g];
+      int rank = 0;
+#pragma unroll 4
+      for (int o = 0; o < p.G; ++o) rank += score[o] > v || (score[o] == v && o < g);
+      if (rank < p.Gk) {
+        kept |= 1u << g;
+        lo = fminf(lo, v);
+      } else {
+        hi = fmaxf(hi, v);
+      }
+    }
+    kept |= __shfl_xor_sync(kFull, kept, 1);
+    kept |= __shfl_xor_sync(kFull, kept, 2);
+    lo = -quad_max(-lo);
+    hi = quad_max(hi);
+    near_group = hi > -INFINITY && lo - hi < 2.0f * eps;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      if (q + 4 * i < sh.nb && !(kept >> ((q + 4 * i) / sh.nbg) & 1u)) top[i] = -INFINITY;
+  }
+
+  // ---- k picks; the round after the last only looks how close the next one was
+  int* ids = reinterpret_cast<int*>(row_id);
+  float prev = INFINITY, vk = INFINITY;  // the pick before; the last one
+  for (int s = 0; s <= p.k; ++s) {
+    float best = top[0];
+    int wb = q;
+#pragma unroll
+    for (int i = 1; i < NB; ++i) {
+      wb = top[i] > best ? q + 4 * i : wb;
+      best = fmaxf(best, top[i]);
+    }
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      const float ob = __shfl_xor_sync(kFull, best, off);
+      const int ow = __shfl_xor_sync(kFull, wb, off);
+      if (ob > best || (ob == best && ow < wb)) {
+        best = ob;
+        wb = ow;
+      }
+    }
+    const bool any = best > -INFINITY;
+    near |= any && prev - best < eps;
+    prev = best;
+    if (s == p.k) break;
+    vk = any ? best : vk;
+    // the block, four columns per thread (a row without candidates looks at its own block 0)
+    if (!any) wb = 0;
+    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (4 * q < sh.bl) v = *reinterpret_cast<const float4*>(row_c + wb * sh.blp + 4 * q);
+    int at = v.x == best ? 0 : v.y == best ? 1 : v.z == best ? 2 : v.w == best ? 3 : 99;
+    at += 4 * q;
+    at = min(at, __shfl_xor_sync(kFull, at, 1));
+    at = min(at, __shfl_xor_sync(kFull, at, 2));
+    const int mine = at - 4 * q;
+    const float rest = quad_max(fmaxf(fmaxf(mine == 0 ? -INFINITY : v.x, mine == 1 ? -INFINITY : v.y),
+                                      fmaxf(mine == 2 ? -INFINITY : v.z, mine == 3 ? -INFINITY : v.w)));
+    if (any && mine >= 0 && mine < 4) row_c[wb * sh.blp + at] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      if (any && wb == q + 4 * i) top[i] = rest;
+    if (q == 0) ids[s] = any ? 16 * wb + at : -1;
+    __syncwarp();
+  }
+  __syncwarp();
+  for (int s = q; s < p.k; s += 4)  // places -> columns
+    if (ids[s] >= 0) ids[s] = ids[s] / 16 / sh.nbg * sh.gs + ids[s] / 16 % sh.nbg * sh.bl + ids[s] % 16;
+  __syncwarp();
+  // rows that fp32 could not decide: the warp takes them one by one
+  if (__any_sync(kFull, (near || near_group) && live)) {
+    const int lanes_g = sh.gs / NC;
+    const bool runs = p.G > 1 && sh.gs % NC == 0 && (lanes_g & (lanes_g - 1)) == 0;
+    for (unsigned todo = __ballot_sync(kFull, (near || near_group) && live && q == 0); todo; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1;  // the row's first lane
+      const int rr = (threadIdx.x - lane + from) / 4;
+      const T* other = static_cast<const T*>(p.logits) + (t - r + rr) * p.stride;
+      bool whole = __shfl_sync(kFull, near_group, from);
+      int id = -1;
+      const uint32_t groups = __shfl_sync(kFull, kept, from);
+      const float thr = __shfl_sync(kFull, vk - eps, from), om = __shfl_sync(kFull, m, from);
+      const float oinv = __shfl_sync(kFull, inv, from);
+      if (!whole) whole = pick_near<T>(p, other, lane, groups, thr, om, oinv, &exact[0], &id) > 32;
+      if (whole) id = pick_exact<T, NC>(p, other, lane, runs, lanes_g, &exact[0], &exact[1]);
+      if (lane < p.k) reinterpret_cast<int*>(s_bias + 16 * sh.nb)[rr * kMaxTopK + lane] = id;
+      __syncwarp();
+    }
+  }
+
+  // ---- weights: thread q takes the slots q, q + 4, ...
+  float l[kMaxTopK / 4], most = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxTopK / 4; ++i) {
+    const int s = q + 4 * i;
+    l[i] = s < p.k && ids[s] >= 0 ? usable<T>(Elem<T>::to_f(row[ids[s]])) : -INFINITY;
+    most = fmaxf(most, l[i]);
+  }
+  most = quad_max(most);
+#pragma unroll
+  for (int i = 0; i < kMaxTopK / 4; ++i)
+    if (4 * i < p.k) {
+      l[i] = picked_score(p.sigmoid, p.renorm, l[i], most, m, z);
+      sum += l[i];
+    }
+  sum += __shfl_xor_sync(kFull, sum, 1);
+  sum += __shfl_xor_sync(kFull, sum, 2);
+  const float f = !p.renorm ? p.scale : sum > 0.f ? p.scale / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxTopK / 4; ++i) {
+    const int s = q + 4 * i;
+    if (live && s < p.k) {
+      p.ids[t * p.k + s] = ids[s];
+      p.w[t * p.k + s] = l[i] * f;
     }
   }
 }
@@ -566,10 +964,14 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const RouteArgs p)
 // The ids carry no gradient, and neither does the bias.  One warp per row,
 // everything in fp32, one rounding to the logits' type at the store.  Bound by
 // the row's bytes: the logits are read whole only where p is needed.
+template <int NC>
+constexpr int kBackwardBlocks = NC <= 2 ? 12 : NC <= 4 ? 10 : NC == 8 ? 8 : NC == 16 ? 5 : 3;  // resident per SM
 template <typename T, int NC>
-__global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBackwardArgs p) {
+__global__ void __launch_bounds__(kThreads, kBackwardBlocks<NC>) route_backward_kernel(const __grid_constant__ RouteBackwardArgs p) {
   const int lane = threadIdx.x % 32;
   const int c0 = lane * NC;
+  __shared__ __align__(16) float s_row[kWarps][32 * NC];
+  float* row_sm = s_row[threadIdx.x / 32];
   const T* __restrict__ logits = static_cast<const T*>(p.logits);
   T* __restrict__ grad = static_cast<T*>(p.grad);
   const int64_t step = (int64_t)gridDim.x * kWarps;
@@ -577,6 +979,19 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
   if (t >= p.T) return;
 
   const bool dense = p.balance != 0.f || p.z != 0.f || (!p.sigmoid && !p.renorm && p.grad_w);
+  const float cb = p.balance * (float)p.E / (float)p.T, cz = 2.0f * p.z / (float)p.T;
+  // a row's inputs, fetched one row ahead
+  float nv[NC], ng = 0.f;
+  int nid = -1;
+  auto fetch = [&](int64_t row_t) {
+    if (dense) load_cols<T, NC>(logits + row_t * p.stride, c0, p.E, p.vec, nv);
+    if (p.grad_w) {
+      nid = lane < p.k ? p.ids[row_t * p.k + lane] : -1;
+      ng = lane < p.k ? p.grad_w[row_t * p.k + lane] * p.scale : 0.f;
+    }
+  };
+  fetch(t);
+
   float f[NC];
 #pragma unroll
   for (int j = 0; j < NC; ++j) f[j] = 0.f;
@@ -588,91 +1003,107 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
       f[j] = (float)c;
       n += c;
     }
-    n = warp_sum(n);
+    // in two parts that the warp's integer sum takes
+    n = ((int64_t)__reduce_add_sync(kFull, (int)(n >> 16)) << 16) + __reduce_add_sync(kFull, (unsigned)(n & 0xffff));
     const float inv = n > 0 ? (float)(1.0 / (double)n) : 0.f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) f[j] *= inv;
   }
-  const float cb = p.balance * (float)p.E / (float)p.T, cz = 2.0f * p.z / (float)p.T;
 
   for (; t < p.T; t += step) {
     const T* row = logits + t * p.stride;
-    int id = lane < p.k && p.grad_w ? p.ids[t * p.k + lane] : -1;
-    if (id >= p.E) id = -1;
-    const float g = id >= 0 ? p.grad_w[t * p.k + lane] * p.scale : 0.f;
-    const float l = id >= 0 ? usable<T>(Elem<T>::to_f(row[id])) : -INFINITY;
-
+    const int id = nid >= 0 && nid < p.E ? nid : -1;
+    const float g = id >= 0 ? ng : 0.f;
     float v[NC];
-    float m = 0.f, z = 1.f;
 #pragma unroll
-    for (int j = 0; j < NC; ++j) v[j] = 0.f;
-    if (dense) {
-      load_cols<T, NC>(row, c0, p.E, p.vec, v);
-      m = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        v[j] = usable<T>(v[j]);
-        m = fmaxf(m, v[j]);
-      }
-      m = warp_max(m);
-      z = 0.f;
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        v[j] = v[j] > -INFINITY ? expf(v[j] - m) : 0.f;
-        z += v[j];
-      }
-      z = warp_sum(z);
-    }
+    for (int j = 0; j < NC; ++j) v[j] = dense ? usable<T>(nv[j]) : 0.f;
+    const float l = id >= 0 ? usable<T>(Elem<T>::to_f(row[id])) : -INFINITY;
+    if (t + step < p.T) fetch(t + step);
 
-    // ---- the picked slots (lane s < k)
+    // ---- maxima of the row and of the picks, then all sums in one pass
+    float m = 0.f, top = 0.f, z = 0.f, fp = 0.f;
+    if (dense) {
+      m = v[0];
+#pragma unroll
+      for (int j = 1; j < NC; ++j) m = fmaxf(m, v[j]);
+      m = warp_max(m);
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        v[j] = v[j] > -INFINITY ? exp_near(v[j] - m) : 0.f;
+        z += v[j];
+        fp = fmaf(f[j], v[j], fp);
+      }
+    }
+    // picked slots (lane s < k): q its score, up to a factor of the row where the weights are renormalised
+    const bool whole = !p.sigmoid && !p.renorm;  // probabilities as they are
+    float q = 0.f;
+    if (p.grad_w) {
+      if (!whole) top = p.renorm ? warp_max(l) : 0.f;
+      q = whole ? (l > -INFINITY ? exp_near(l - m) : 0.f) : picked_score(p.sigmoid, p.renorm, l, top, 0.f, 1.f);
+    }
+    float S = q, D = q * g;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      z += __shfl_xor_sync(kFull, z, off);
+      fp += __shfl_xor_sync(kFull, fp, off);
+      S += __shfl_xor_sync(kFull, S, off);
+      D += __shfl_xor_sync(kFull, D, off);
+    }
+    const float inv = z > 0.f ? rcp_near(z) : 0.f;
     float part = 0.f, shared = 0.f;  // shared: what every p_i is multiplied with
     if (p.grad_w) {
-      if (!p.sigmoid && !p.renorm) {
-        const float pw = z > 0.f && l > -INFINITY ? expf(l - m) / z : 0.f;
-        part = pw * g;
-        shared = -warp_sum(part);
+      const float rest = p.sigmoid && l > -INFINITY ? rcp_near(1.0f + exp_near(l)) : 1.0f;  // 1 - sigmoid(l)
+      if (whole) {
+        part = q * inv * g;
+        shared = -D * inv;
+      } else if (p.renorm) {
+        const float is = S > 0.f ? rcp_near(S) : 0.f;
+        part = q * is * rest * (g - D * is);
       } else {
-        const float top = warp_max(l);
-        float q = picked_score(p.sigmoid, p.renorm, l, top, 0.f, 1.f);
-        const float rest = p.sigmoid && l > -INFINITY ? 1.0f / (1.0f + expf(l)) : 1.0f;  // 1 - sigmoid(l)
-        if (p.renorm) {
-          const float sum = warp_sum(q);
-          q = sum > 0.f ? q / sum : 0.f;
-          part = q * rest * (g - warp_sum(q * g));
-        } else {
-          part = q * rest * g;
-        }
+        part = q * rest * g;
       }
     }
     if (dense) {
-      const float inv = z > 0.f ? 1.0f / z : 0.f;
-#pragma unroll
-      for (int j = 0; j < NC; ++j) v[j] *= inv;
-      float fp = 0.f;
-      if (p.balance != 0.f) {
-#pragma unroll
-        for (int j = 0; j < NC; ++j) fp = fmaf(f[j], v[j], fp);
-        fp = warp_sum(fp);
-      }
       if (p.z != 0.f && z > 0.f) shared += cz * (m + logf(z));
+      const float mean = fp * inv;
 #pragma unroll
-      for (int j = 0; j < NC; ++j) v[j] *= fmaf(cb, f[j] - fp, shared);
+      for (int j = 0; j < NC; ++j) v[j] = v[j] * inv * fmaf(cb, f[j] - mean, shared);
     }
     if (p.grad_w) {
-      for (int s = 0; s < p.k; ++s) {
-        const int at = __shfl_sync(kFull, id, s) - c0;
-        const float add = __shfl_sync(kFull, part, s);
+      // the picks' parts join the row in shared memory, repeated ids one after the other
+      float* mine = row_sm + c0;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) v[j] += at == j ? add : 0.f;
+      for (int j = 0; j < NC; ++j) mine[j] = v[j];
+      const unsigned same = __match_any_sync(kFull, id) & ((1u << lane) - 1u);
+      const bool valid = id >= 0;
+      __syncwarp();
+      if (valid && same == 0) row_sm[id] += part;
+      __syncwarp();
+      if (__any_sync(kFull, valid && same != 0)) {
+        for (int s = 1; s < p.k; ++s) {
+          if (lane == s && valid && same != 0) row_sm[id] += part;
+          __syncwarp();
+        }
       }
+#pragma unroll
+      for (int j = 0; j < NC; ++j) v[j] = mine[j];
     }
     store_cols<T, NC>(grad + t * p.stride, c0, p.E, p.vec, v);
   }
 }
 
+// From this many rows (and up to 512 experts) four threads per row instead of a
+// warp: fewer instructions, a longer chain.  Measured, us, warp / four threads:
+//   rows    256 fp32, sigmoid in groups, k 8   128 bf16, softmax, k 4   8 fp32, k 2
+//   1024    8.2 / 13.7                         3.7 / 4.8                3.3 / 3.7
+//   4096    13.8 / 16.7                        4.9 / 4.9                4.0 / 3.6
+//   8192    19.8 / 18.9                        8.9 / 6.3                6.6 / 3.8
+//   65536   102 / 55                           54 / 16.5                42 / 11.4
+constexpr int64_t kTileMinRows = 8192;
+
 // Blocks: a warp per row up to a few resident blocks per SM, then rows in turn
-unsigned blocks_for(int64_t T) {
-  const int64_t cap = (int64_t)device_sm_count() * 12;
+unsigned blocks_for(int64_t T, int per_sm) {
+  const int64_t cap = (int64_t)device_sm_count() * per_sm;
   const int64_t n = (T + kWarps - 1) / kWarps;
   return (unsigned)(n < cap ? n : cap);
 }
@@ -701,7 +1132,21 @@ cudaError_t launch_route_topk(const RouteArgs& args, cudaStream_t stream) {
   auto typed = [&](auto tag) {
     using T = decltype(tag);
     return by_columns<T>(a.E, [&](auto nc) {
-      route_topk_kernel<T, decltype(nc)::value><<<blocks_for(a.T), kThreads, 0, stream>>>(a);
+      constexpr int NC = decltype(nc)::value;
+      if constexpr (NC <= 16) {
+        if (a.T >= kTileMinRows && tile_shape(a.E, a.G).nb <= 4 * kTileBlocks<NC>) {
+          const size_t smem = tile_smem(a.E, a.G);
+          if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(route_tile_kernel<T, NC>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+          }
+          route_tile_kernel<T, NC>
+              <<<(unsigned)((a.T + kTileRows - 1) / kTileRows), kThreads, smem, stream>>>(a);
+          return cudaGetLastError();
+        }
+      }
+      route_topk_kernel<T, decltype(nc)::value><<<blocks_for(a.T, 12), kThreads, 0, stream>>>(a);
       return cudaGetLastError();
     });
   };
@@ -717,7 +1162,7 @@ cudaError_t launch_route_backward(const RouteBackwardArgs& args, cudaStream_t st
   auto typed = [&](auto tag) {
     using T = decltype(tag);
     return by_columns<T>(a.E, [&](auto nc) {
-      route_backward_kernel<T, decltype(nc)::value><<<blocks_for(a.T), kThreads, 0, stream>>>(a);
+      route_backward_kernel<T, decltype(nc)::value><<<blocks_for(a.T, kBackwardBlocks<decltype(nc)::value>), kThreads, 0, stream>>>(a);
       return cudaGetLastError();
     });
   };
