@@ -90,7 +90,7 @@ class Case:
         return self
 
     def plan(self, stream=None):
-        p = torch.full((moe.moe_adapter_plan_bytes(self.cfg, self.ad),), 0xAB, dtype=torch.uint8, device="cuda")
+        p = torch.full((moe.moe_adapter_plan_bytes(self.cfg, self.ad),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN wherever nothing is written
         moe.moe_adapter_plan(self.cfg, self.ad, self.offsets, self.perm, self.ta, p, stream=stream)
         return p
 
@@ -270,7 +270,7 @@ def _forward(cfg, route, t, ad=None, names=("w_gu", "w_d", "s_gu", "s_d")):
     ids = torch.empty(cfg.T, cfg.top_k, dtype=torch.int32, device="cuda")
     w = torch.empty(cfg.T, cfg.top_k, device="cuda")
     counts = torch.empty(cfg.n_experts, dtype=torch.int32, device="cuda")
-    ws = torch.full((max(256, moe.moe_forward_routed_workspace_bytes(cfg, ad)),), 0xAB, dtype=torch.uint8,
+    ws = torch.full((max(256, moe.moe_forward_routed_workspace_bytes(cfg, ad)),), 0xFF, dtype=torch.uint8,
                     device="cuda")
     moe.moe_forward_routed(cfg, route, ad, t["x"], t["logits"], None, *(t[n] for n in names), y, ids, w, counts, ws)
     return y, ids, w, counts, ws

@@ -42,12 +42,20 @@ constexpr unsigned kFull = 0xffffffffu;
 static_assert((int64_t)(kAdapterMaxPairs + 1) * kChunkRows < (int64_t(1) << 31), "keys of the plan are 31 bits");
 constexpr int kSkip = 0x7fffff;  // pair of a row that is not there (kMaxPairs - 1 is below)
 
-struct Tile {
-  int start;    // first position in `order`
+struct __align__(16) Tile {
+  int start;    // position of its first row among the grouped rows: where its U lies
   int count;    // rows
   int adapter;  // -1: none
   int expert;
+  int rows[kTileRows];
 };
+struct TileHead {  // in registers
+  int start, count, adapter, expert;
+};
+__device__ __forceinline__ TileHead head_of(const Tile* t) {
+  const int4 v = *reinterpret_cast<const int4*>(t);
+  return TileHead{v.x, v.y, v.z, v.w};
+}
 
 // ---------------------------------------------------------------- plan
 struct PlanParams {
@@ -56,10 +64,10 @@ struct PlanParams {
   const int32_t* token_adapter;
   int64_t rows;
   int E, k, N;
-  int32_t* order;
   Tile* tiles;
   int* n_tiles;
   int* status;
+  bool clear;  // one block: the status word is this call's own
 };
 
 // Four threads per row: each compares the row's key with a quarter of the
@@ -70,7 +78,7 @@ constexpr int kPlanThreads = 4 * kChunkRows;
 __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanParams p) {
   extern __shared__ int s_off[];  // [E+1]
   __shared__ __align__(16) int keys[kChunkRows];
-  __shared__ int sorted[kChunkRows];
+  __shared__ int sorted[kChunkRows], s_row[kChunkRows];
   __shared__ int warp_sums[kChunkRows / 32];
   __shared__ int s_base;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -79,6 +87,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
   const int64_t row0 = (int64_t)blockIdx.x * kChunkRows;
   const int64_t row = row0 + tid;
   const bool mine_to_load = tid < kChunkRows && row < p.rows;
+  bool bad = false;
   const int slot = mine_to_load && p.perm ? p.perm[row] : 0;  // garbage behind the last row: not used there
   if (p.offsets)
     for (int e = tid; e <= p.E; e += kPlanThreads) s_off[e] = p.offsets[e];
@@ -89,7 +98,7 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
     if (row < live) {
       int a = p.token_adapter[p.perm ? slot / p.k : row];
       if (a >= p.N) {
-        set_status(p.status, kDevBadAdapterId);
+        bad = true;
         a = -1;
       }
       int e = 0;
@@ -121,15 +130,19 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
     rank += __shfl_xor_sync(kFull, rank, 2);
     if (quarter == 0) {
       sorted[rank] = key / kChunkRows;
-      if (key / kChunkRows != kSkip) p.order[row0 + rank] = (int32_t)(row0 + i);
+      s_row[rank] = (int)(row0 + i);
     }
   }
-  __syncthreads();
+  bad = __syncthreads_or(bad);
+  if (tid == 0) {
+    if (p.clear) *p.status = bad ? kDevBadAdapterId : 0;
+    else if (bad) set_status(p.status, kDevBadAdapterId);
+  }
   // position tid of the sorted chunk starts a tile where its run starts, and
   // every kTileRows from there
   const int mine = tid < kChunkRows ? sorted[tid] : kSkip;
   bool head = false;
-  int end = 0;
+  int end = 0, place = 0;  // place: in its tile
   if (mine != kSkip) {
     int lo = 0, hi = tid;  // first position of the run (the pairs ascend)
     while (lo < hi) {
@@ -137,7 +150,8 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
       if (sorted[mid] < mine) lo = mid + 1;
       else hi = mid;
     }
-    head = (tid - lo) % kTileRows == 0;
+    place = (tid - lo) % kTileRows;
+    head = place == 0;
     if (head) {
       lo = tid + 1;
       hi = min(kChunkRows, tid + kTileRows);
@@ -159,13 +173,20 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
       warp_sums[w] = n;
       n += c;
     }
-    s_base = n ? atomicAdd(p.n_tiles, n) : 0;  // the order of the tiles changes no result
+    s_base = 0;  // the order of the tiles changes no result
+    if (gridDim.x == 1) *p.n_tiles = n;
+    else if (n) s_base = atomicAdd(p.n_tiles, n);
   }
   __syncthreads();
-  if (head) {
-    const int at = s_base + warp_sums[warp] + __popc(heads & ((1u << lane) - 1u));
-    const int pair = mine - 1;
-    p.tiles[at] = Tile{(int)(row0 + tid), end - tid, pair < 0 ? -1 : pair % p.N, pair < 0 ? 0 : pair / p.N};
+  if (mine != kSkip) {
+    // the tile of a position: the heads up to it, less one
+    Tile* tile = p.tiles + s_base + warp_sums[warp] + __popc(heads & (0xffffffffu >> (31 - lane))) - 1;
+    tile->rows[place] = s_row[tid];
+    if (head) {
+      const int pair = mine - 1;
+      *reinterpret_cast<int4*>(tile) =
+          make_int4((int)(row0 + tid), end - tid, pair < 0 ? -1 : pair % p.N, pair < 0 ? 0 : pair / p.N);
+    }
   }
 }
 
@@ -173,14 +194,64 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
 struct ShrinkParams {
   const void* x;  // [rows, K]
   const void* a;  // [N, E, r, K]
-  const int32_t* order;
   const Tile* tiles;
   const int* n_tiles;
-  float* u;       // [S][rows][r] by position in `order`
-  int64_t rows;
+  float* u;       // [rows][r]: a tile's first partial sum, by tile.start
+  float* more;    // [blocks][16][r]: the partial sums that continue a tile
   int K, r, E;
-  int k_block;    // inputs per block (blockIdx.y)
 };
+
+// The work is a list of units, kUnits of 512 inputs per tile, and every block
+// takes an equal run of it.  A run holds whole tiles, and perhaps the end of a
+// tile that an earlier block began and the beginning of one that a later block
+// ends: the partial sum of a beginning goes to the tile's place in u, that of a
+// continuation (a block has one at most) to the block's place in more, and the
+// expand adds them in the order of the blocks.
+constexpr int kUnitInputs = 64 * kWarps;
+// a / b for a >= 0: 64-bit divisions are slow, and the numbers seldom need them
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+struct Run {
+  int64_t lo, hi;
+};
+// With fewer units than blocks only so many blocks take part: no run between two
+// others is empty.
+__device__ __forceinline__ Run run_of(int64_t total, int block, int blocks) {
+  blocks = (int)min((int64_t)blocks, total);
+  if (block >= blocks) return Run{0, 0};
+  return Run{quotient(total * block, blocks), quotient(total * (block + 1), blocks)};
+}
+// the block whose run holds a unit
+__device__ __forceinline__ int block_of(int64_t unit, int64_t total, int blocks) {
+  blocks = (int)min((int64_t)blocks, total);
+  return (int)quotient((unit + 1) * blocks - 1, total);
+}
+// a tile's run of blocks that hold partial sums of it: first..last
+struct Parts {
+  int first, last;
+};
+__device__ __forceinline__ Parts parts_of(int tile, int n_tiles, int units, int blocks) {
+  const int64_t total = (int64_t)n_tiles * units, at = (int64_t)tile * units;
+  return Parts{block_of(at, total, blocks), block_of(at + units - 1, total, blocks)};
+}
+// U[i, k..k+3] of a tile, all partial sums
+__device__ __forceinline__ float4 sum_parts(const float* u, const float* more, int start, Parts parts, int r,
+                                            int i, int k) {
+  float4 v = __ldg(reinterpret_cast<const float4*>(u + (int64_t)(start + i) * r + k));
+#pragma unroll 4
+  for (int b = parts.first + 1; b <= parts.last; ++b) {
+    const float4 w = __ldg(reinterpret_cast<const float4*>(more + ((int64_t)b * kTileRows + i) * r + k));
+    v.x += w.x;
+    v.y += w.y;
+    v.z += w.z;
+    v.w += w.w;
+  }
+  return v;
+}
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -228,17 +299,22 @@ __global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) adapter_shrink_kern
   const uint32_t ring = tc::smem_u32(ring_ptr);
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
-  const int n_tiles = *p.n_tiles;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
-  const int k_lo = blockIdx.y * p.k_block, k_hi = min(p.K, k_lo + p.k_block);
-  for (int t = blockIdx.x; t < n_tiles; t += gridDim.x) {
-    const Tile tile = p.tiles[t];
+  const int units = (p.K + kUnitInputs - 1) / kUnitInputs;
+  const Run run = run_of((int64_t)*p.n_tiles * units, blockIdx.x, gridDim.x);
+  for (int64_t at = run.lo; at < run.hi;) {
+    const int t = (int)quotient(at, units);
+    const int* rows = p.tiles[t].rows;
+    const TileHead tile = head_of(&p.tiles[t]);
+    const int u_lo = (int)(at - (int64_t)t * units), u_hi = (int)min((int64_t)units, u_lo + (run.hi - at));
+    at += u_hi - u_lo;
     if (tile.adapter < 0) continue;
+    const int k_lo = u_lo * kUnitInputs, k_hi = min(p.K, u_hi * kUnitInputs);
     const __nv_bfloat16* a =
         static_cast<const __nv_bfloat16*>(p.a) + ((int64_t)tile.adapter * p.E + tile.expert) * p.r * p.K;
     int64_t row[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) row[h] = h * 8 + g < tile.count ? p.order[tile.start + h * 8 + g] : -1;
+    for (int h = 0; h < 2; ++h) row[h] = h * 8 + g < tile.count ? rows[h * 8 + g] : -1;
     float acc[RT][4];
 #pragma unroll
     for (int n = 0; n < RT; ++n)
@@ -250,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) adapter_shrink_kern
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int k = k0 + 32 * c + 8 * t4;
-        const bool in = k < k_hi;  // K and k_block are multiples of 8
+        const bool in = k < k_hi;  // K is a multiple of 8
 #pragma unroll
         for (int n = 0; n < RT; ++n) {
           const bool on = in && n * 8 + g < p.r;
@@ -311,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) adapter_shrink_kern
       }
     }
     if (warp == 0) {
-      float* u = p.u + ((int64_t)blockIdx.y * p.rows + tile.start) * p.r;
+      float* u = u_lo == 0 ? p.u + (int64_t)tile.start * p.r : p.more + (int64_t)blockIdx.x * kTileRows * p.r;
 #pragma unroll
       for (int n = 0; n < RT; ++n)
 #pragma unroll
@@ -330,13 +406,18 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_f32_kernel(const Shri
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
-  const int n_tiles = *p.n_tiles;
   const float* x = static_cast<const float*>(p.x);
-  const int k_lo = blockIdx.y * p.k_block, k_hi = min(p.K, k_lo + p.k_block);
   const int ranks = p.r / 8;
-  for (int t = blockIdx.x; t < n_tiles; t += gridDim.x) {
-    const Tile tile = p.tiles[t];
+  const int k_units = (p.K + kUnitInputs - 1) / kUnitInputs;
+  const Run run = run_of((int64_t)*p.n_tiles * k_units, blockIdx.x, gridDim.x);
+  for (int64_t at = run.lo; at < run.hi;) {
+    const int t = (int)quotient(at, k_units);
+    const int* rows = p.tiles[t].rows;
+    const TileHead tile = head_of(&p.tiles[t]);
+    const int u_lo = (int)(at - (int64_t)t * k_units), u_hi = (int)min((int64_t)k_units, u_lo + (run.hi - at));
+    at += u_hi - u_lo;
     if (tile.adapter < 0) continue;
+    const int k_lo = u_lo * kUnitInputs, k_hi = min(p.K, u_hi * kUnitInputs);
     const float* a = static_cast<const float*>(p.a) + ((int64_t)tile.adapter * p.E + tile.expert) * p.r * p.K;
     const int units = (tile.count + 3) / 4 * ranks;
     for (int unit = warp; unit < units; unit += kWarps) {
@@ -346,7 +427,7 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_f32_kernel(const Shri
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         on[i] = i0 + i < tile.count;
-        xr[i] = x + (int64_t)p.order[tile.start + (on[i] ? i0 + i : i0)] * p.K;
+        xr[i] = x + (int64_t)rows[on[i] ? i0 + i : i0] * p.K;
       }
       float acc[4][8];
 #pragma unroll
@@ -369,7 +450,8 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_f32_kernel(const Shri
             acc[i][c] = fmaf(xv[i].w, av[c].w, acc[i][c]);
           }
       }
-      float* u = p.u + ((int64_t)blockIdx.y * p.rows + tile.start + i0) * p.r + c0;
+      float* u = (u_lo == 0 ? p.u + (int64_t)tile.start * p.r : p.more + (int64_t)blockIdx.x * kTileRows * p.r) +
+                 (int64_t)i0 * p.r + c0;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -384,16 +466,17 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_f32_kernel(const Shri
 
 // ---------------------------------------------------------------- expand
 struct ExpandParams {
-  const float* u;  // [S][rows][r]
+  const float* u;     // as the shrink left them
+  const float* more;
   const void* b;   // [N, E, n_out, r]
   const float* scale;
   const void* base;  // [rows, n_out]
   void* out;         // [rows, f] (SwiGLU: n_out = 2 f) or [rows, n_out]
-  const int32_t* order;
   const Tile* tiles;
   const int* n_tiles;
   int64_t rows;
-  int r, E, S;
+  int r, E;
+  int units, shrink_blocks;  // the shrink's units per tile and its blocks
   int n_out, n_res;  // columns of base and of the result
   int col_block;     // fp32: result columns per block (blockIdx.x)
   bool in_place;     // base is the result and nothing is applied to it: rows without an adapter are right
@@ -427,11 +510,15 @@ __device__ __forceinline__ float finish_bf16(float v, float up) {
 // The work is a list of rounds: a tile times CW result columns (and, for
 // SwiGLU, the matching up columns), tile after tile; every block takes an equal
 // run of it, so the blocks end together whatever the tiles are.  A producer warp
-// fetches the columns' rows of B (one contiguous piece each) into a ring of
-// stages with bulk copies under mbarriers; eight consumer warps each take 32
-// columns of a round and fetch their part of base themselves, each lane its own 16-byte vectors, a few rounds ahead.  (base by
-// bulk copies as well, a segment of each row, measured 186 against 117 us for
-// 16-byte copies: at 256 bytes a bulk copy costs more than it moves.)
+// goes ahead of eight consumer warps: per tile it sums U, scales it and leaves it
+// as MMA fragments in shared memory with the tile's rows (the eight would
+// otherwise do it eight times, and wait for it), and per round it fetches the
+// columns' rows of B (one contiguous piece each) with bulk copies into a ring of
+// stages under mbarriers.  A consumer warp takes 32 columns of a round and
+// fetches its part of base itself, each lane its own 16-byte vectors, a few
+// rounds ahead and on into the next tile.  (base by bulk copies as well, a
+// segment of each row, measured 186 against 117 us for 16-byte copies: at 256
+// bytes a bulk copy costs more than it moves.)
 //
 // Column 2t+i of instruction j stands for column 8t + 2j + i of the warp's 32, so
 // a lane ends with 8 consecutive columns of a row: base is read and the result
@@ -439,10 +526,20 @@ __device__ __forceinline__ float finish_bf16(float v, float up) {
 // as a sum of two bf16 values (16 bits of mantissa), so its rounding does not
 // show beside the result's own.
 constexpr int kMaxStages = 8;
+constexpr int kInfos = 4;  // tiles the producer may be ahead
 struct ExpandHeader {
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];  // stages of B
+  uint64_t ifull[kInfos], iempty[kInfos];        // tiles
   int fill_par[kMaxStages];
   int abort;
+};
+template <int RK>
+struct __align__(16) TileInfo {
+  int q0, q_end;  // rounds of this block's run
+  int count;      // rows; -1: the run is over
+  int has;        // an adapter
+  int rows[kTileRows];
+  uint4 hi[RK][32], lo[RK][32];  // U, lane by lane: rows g, g + 8; ranks 16 c + 4 t4 + {0, 1} and {2, 3}
 };
 constexpr int kExpandHead = 256;
 static_assert(sizeof(ExpandHeader) <= kExpandHead, "header of the expand ring");
@@ -469,18 +566,26 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, int byt
 }
 
 template <int RK, int EPI>
-__global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>()) adapter_expand_kernel(const ExpandParams p) {
+__global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
+    adapter_expand_kernel(const __grid_constant__ ExpandParams p) {
   using Sh = ExpandShape<EPI>;
   constexpr int H = Sh::H, CW = Sh::CW;
   extern __shared__ __align__(16) uint8_t smem[];
   ExpandHeader* hd = reinterpret_cast<ExpandHeader*>(smem);
-  uint8_t* ring = smem + kExpandHead + Sh::kBase;
+  TileInfo<RK>* infos = reinterpret_cast<TileInfo<RK>*>(smem + kExpandHead);
+  uint8_t* bases = smem + kExpandHead + kInfos * sizeof(TileInfo<RK>);
+  uint8_t* ring = bases + Sh::kBase;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int g = lane / 4, t4 = lane % 4;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       tc::mbar_init(tc::smem_u32(&hd->full[i]), 1);
       tc::mbar_init(tc::smem_u32(&hd->empty[i]), kWarps);
       hd->fill_par[i] = -1;
+    }
+    for (int i = 0; i < kInfos; ++i) {
+      tc::mbar_init(tc::smem_u32(&hd->ifull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&hd->iempty[i]), kWarps);
     }
     hd->abort = 0;
     tc::fence_mbar_init();
@@ -489,26 +594,80 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>()) adap
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   volatile int* abort_flag = &hd->abort;
-  const int rounds = (p.n_res + CW - 1) / CW;  // per tile
-  const int64_t total = (int64_t)*p.n_tiles * rounds;
-  const int64_t lo_round = total * blockIdx.x / gridDim.x, hi_round = total * (blockIdx.x + 1) / gridDim.x;
   const int b_bytes = CW * p.r * 2;
-  int stage = 0;
-  uint32_t phase = 0;
+  int stage = 0, info = 0;  // stages and tiles in turn, with their parities
+  uint32_t phase = 0, info_phase = 0;
 
   if (warp == kWarps) {
-    // ------------------------------------------------ producer (one lane)
-    if (lane == 0) {
-      bool ok = true;
-      for (int64_t at = lo_round; ok && at < hi_round;) {
-        const Tile tile = p.tiles[at / rounds];
-        int q = (int)(at % rounds);
-        const int q_end = (int)min((int64_t)rounds, q + (hi_round - at));
-        at += q_end - q;
-        if (tile.adapter < 0) continue;
+    // ------------------------------------------------ producer
+    const int rounds = (p.n_res + CW - 1) / CW;  // per tile
+    const int n_tiles = *p.n_tiles;
+    const Run run = run_of((int64_t)n_tiles * rounds, blockIdx.x, gridDim.x);
+    for (int64_t at = run.lo;;) {
+      const bool over = at >= run.hi;
+      const int t = over ? 0 : (int)quotient(at, rounds);
+      const TileHead tile = over ? TileHead{0, -1, -1, 0} : head_of(&p.tiles[t]);
+      const int q0 = over ? 0 : (int)(at - (int64_t)t * rounds);
+      const int q_end = over ? 0 : (int)min((int64_t)rounds, q0 + (run.hi - at));
+      at += q_end - q0;
+      const bool has = tile.adapter >= 0;
+      if (!over && !has && p.in_place) continue;
+      const int row = !over && lane < tile.count ? p.tiles[t].rows[lane & (kTileRows - 1)] : 0;
+      float4 u[RK][2];
+      if (has) {
+        const Parts parts = parts_of(t, n_tiles, p.units, p.shrink_blocks);
+        const float sc = p.scale[tile.adapter];
+#pragma unroll
+        for (int c = 0; c < RK; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            u[c][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int i = h * 8 + g, k = 16 * c + 4 * t4;
+            if (i < tile.count && k < p.r) {
+              const float4 v = sum_parts(p.u, p.more, tile.start, parts, p.r, i, k);
+              u[c][h] = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
+            }
+          }
+      }
+      int ok = 0;
+      if (lane == 0)
+        ok = tc::mbar_wait_bounded(tc::smem_u32(&hd->iempty[info]), info_phase ^ 1u, abort_flag, p.wait_limit_ns,
+                                   p.status);
+      if (!__shfl_sync(kFull, ok, 0)) break;
+      TileInfo<RK>& to = infos[info];
+      if (lane == 0) *reinterpret_cast<int4*>(&to) = make_int4(q0, q_end, tile.count, has);
+      if (lane < kTileRows) to.rows[lane] = row;
+      if (has) {
+#pragma unroll
+        for (int c = 0; c < RK; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 v = u[c][h];
+            hi[h] = pack_bf16x2(v.x, v.y);
+            hi[2 + h] = pack_bf16x2(v.z, v.w);
+            const __nv_bfloat162 p0 = *reinterpret_cast<__nv_bfloat162*>(&hi[h]);
+            const __nv_bfloat162 p1 = *reinterpret_cast<__nv_bfloat162*>(&hi[2 + h]);
+            lo[h] = pack_bf16x2(v.x - __low2float(p0), v.y - __high2float(p0));
+            lo[2 + h] = pack_bf16x2(v.z - __low2float(p1), v.w - __high2float(p1));
+          }
+          to.hi[c][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          to.lo[c][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&hd->ifull[info]));
+      if (++info == kInfos) {
+        info = 0;
+        info_phase ^= 1u;
+      }
+      if (over) break;
+      if (!has) continue;
+      ok = 1;
+      if (lane == 0) {
         const __nv_bfloat16* b =
             static_cast<const __nv_bfloat16*>(p.b) + ((int64_t)tile.adapter * p.E + tile.expert) * p.n_out * p.r;
-        for (; q < q_end; ++q) {
+        for (int q = q0; q < q_end; ++q) {
           const int c0 = q * CW, cols = min(CW, p.n_res - c0);
           const uint32_t full = tc::smem_u32(&hd->full[stage]);
           ok = tc::mbar_wait_bounded(tc::smem_u32(&hd->empty[stage]), phase ^ 1u, abort_flag, p.wait_limit_ns,
@@ -526,84 +685,91 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>()) adap
           }
         }
       }
+      if (!__shfl_sync(kFull, ok, 0)) break;
     }
   } else {
     // ------------------------------------------------ consumers
     const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.base);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-    const int g = lane / 4, t4 = lane % 4;
-    const int w0 = warp * 32;  // this warp's columns of a round
-    const uint8_t* mine = smem + kExpandHead + warp * (Sh::kAhead * Sh::kSlot) + lane * 16;
+    const int w0 = warp * 32 + 8 * t4;  // this lane's first column of a round
+    const uint8_t* mine = bases + warp * (Sh::kAhead * Sh::kSlot) + lane * 16;
     const uint32_t mine32 = tc::smem_u32(mine);
+    // fetching runs ahead of computing: its own place in the tiles
+    int f_info = 0, f_q = 0, f_end = 0, f_slot = 0, ahead = 0;  // ahead: rounds fetched and not yet computed
+    uint32_t f_phase = 0;
+    bool f_over = false, f_on[2] = {false, false};
+    const __nv_bfloat16* src[2][H];
+    // one more round of base, if its tile is known; a group of copies of its own
+    auto fetch = [&]() -> bool {
+      if (f_q == f_end) {
+        const int known = lane == 0 ? (int)tc::mbar_try_wait(tc::smem_u32(&hd->ifull[f_info]), f_phase) : 0;
+        if (!__shfl_sync(kFull, known, 0)) return false;
+        const TileInfo<RK>& ti = infos[f_info];
+        if (ti.count < 0) {
+          f_over = true;
+          return false;
+        }
+        f_q = ti.q0;
+        f_end = ti.q_end;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          f_on[i] = i * 8 + g < ti.count;
+          const int64_t row = f_on[i] ? ti.rows[i * 8 + g] : 0;
+#pragma unroll
+          for (int h = 0; h < H; ++h) src[i][h] = base + row * p.n_out + h * p.n_res + f_q * CW + w0;
+        }
+        if (++f_info == kInfos) {
+          f_info = 0;
+          f_phase ^= 1u;
+        }
+      }
+      const bool in = f_q * CW + w0 < p.n_res;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          copy16(mine32 + f_slot * Sh::kSlot + (i * H + h) * 512, src[i][h], in && f_on[i]);
+          src[i][h] += CW;
+        }
+      copies_commit();
+      ++f_q;
+      ++ahead;
+      f_slot = (f_slot + 1) % Sh::kAhead;
+      return true;
+    };
+    int slot = 0;
     bool ok = true;
-    for (int64_t at = lo_round; ok && at < hi_round;) {
-      const Tile tile = p.tiles[at / rounds];
-      const int q0 = (int)(at % rounds);
-      const int q_end = (int)min((int64_t)rounds, q0 + (hi_round - at));
-      at += q_end - q0;
-      const bool has = tile.adapter >= 0;
-      if (!has && p.in_place) continue;
+    while (ok) {
+      ok = tc::mbar_wait_bounded(tc::smem_u32(&hd->ifull[info]), info_phase, abort_flag, p.wait_limit_ns, p.status);
+      if (!ok) break;
+      const TileInfo<RK>& ti = infos[info];
+      const int4 head = *reinterpret_cast<const int4*>(&ti);
+      if (head.z < 0) break;
+      const bool has = head.w != 0;
       __nv_bfloat16* orow[2];
-      const __nv_bfloat16* src[2][H];  // this lane's vectors of the next round to fetch
       bool on[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        on[i] = i * 8 + g < tile.count;
-        const int64_t row = on[i] ? p.order[tile.start + i * 8 + g] : 0;
-        orow[i] = out + row * p.n_res + w0 + 8 * t4;
-#pragma unroll
-        for (int h = 0; h < H; ++h) src[i][h] = base + row * p.n_out + h * p.n_res + q0 * CW + w0 + 8 * t4;
+        on[i] = i * 8 + g < head.z;
+        orow[i] = out + (on[i] ? (int64_t)ti.rows[i * 8 + g] * p.n_res : 0) + w0;
       }
-      auto issue = [&](int q, int slot) {
-        const bool in = q * CW + w0 + 8 * t4 < p.n_res;
+      uint4 hi[RK], lo[RK];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            copy16(mine32 + slot * Sh::kSlot + (i * H + h) * 512, src[i][h], in && on[i]);
-            src[i][h] += CW;
-          }
-      };
-#pragma unroll
-      for (int d = 0; d < Sh::kAhead - 1; ++d) {
-        if (q0 + d < q_end) issue(q0 + d, d);
-        copies_commit();
+      for (int c = 0; c < RK; ++c) {
+        hi[c] = has ? ti.hi[c][lane] : make_uint4(0, 0, 0, 0);
+        lo[c] = has ? ti.lo[c][lane] : make_uint4(0, 0, 0, 0);
       }
-      uint32_t hi[RK][4], lo[RK][4];  // U fragments: rows g, g+8; ranks 16 c + 4 t4 + {0,1} and {2,3}
-      const float sc = has ? p.scale[tile.adapter] : 0.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int c = 0; c < RK; ++c) {
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          const int k = 16 * c + 4 * t4;
-          if (has && on[h] && k < p.r) {
-            const float* u = p.u + (int64_t)(tile.start + h * 8 + g) * p.r + k;
-#pragma unroll 4
-            for (int s = 0; s < p.S; ++s) {
-              const float4 w = __ldg(reinterpret_cast<const float4*>(u + (int64_t)s * p.rows * p.r));
-              v.x += w.x;
-              v.y += w.y;
-              v.z += w.z;
-              v.w += w.w;
-            }
-            v = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
-          }
-          hi[c][h] = pack_bf16x2(v.x, v.y);
-          hi[c][2 + h] = pack_bf16x2(v.z, v.w);
-          const __nv_bfloat162 p0 = *reinterpret_cast<__nv_bfloat162*>(&hi[c][h]);
-          const __nv_bfloat162 p1 = *reinterpret_cast<__nv_bfloat162*>(&hi[c][2 + h]);
-          lo[c][h] = pack_bf16x2(v.x - __low2float(p0), v.y - __high2float(p0));
-          lo[c][2 + h] = pack_bf16x2(v.z - __low2float(p1), v.w - __high2float(p1));
+      for (int q = head.x; q < head.y; ++q) {
+        while (ahead < Sh::kAhead && !f_over && fetch()) {
         }
-      }
-      int slot = 0;
-      for (int q = q0; q < q_end; ++q) {
-        if (q + Sh::kAhead - 1 < q_end) issue(q + Sh::kAhead - 1, (slot + Sh::kAhead - 1) % Sh::kAhead);
-        copies_commit();
-        copies_wait<Sh::kAhead - 1>();
+        // this round's copies are the oldest of `ahead` groups
+        static_assert(Sh::kAhead == 4, "one wait per depth");
+        if (ahead == 4) copies_wait<3>();
+        else if (ahead == 3) copies_wait<2>();
+        else if (ahead == 2) copies_wait<1>();
+        else copies_wait<0>();
         const int c0 = q * CW;
-        const bool work = c0 + w0 < p.n_res;
+        const bool work = c0 + warp * 32 < p.n_res;
         float acc[H][4][4];
         if (work) {
 #pragma unroll
@@ -621,11 +787,13 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>()) adap
           }
         }
         slot = (slot + 1) % Sh::kAhead;
+        --ahead;
         if (has) {
           ok = tc::mbar_wait_bounded(tc::smem_u32(&hd->full[stage]), phase, abort_flag, p.wait_limit_ns, p.status);
           if (!ok) break;
           if (work) {
-            const uint8_t* st = ring + stage * p.stage_bytes + (w0 + 8 * (g / 2) + (g & 1)) * p.r * 2 + 8 * t4;
+            const uint8_t* st =
+                ring + stage * p.stage_bytes + (warp * 32 + 8 * (g / 2) + (g & 1)) * p.r * 2 + 8 * t4;
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -634,8 +802,8 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>()) adap
 #pragma unroll
                 for (int c = 0; c < RK; ++c) {
                   const uint2 bv = 16 * c + 4 * t4 < p.r ? *reinterpret_cast<const uint2*>(sb + 32 * c) : make_uint2(0, 0);
-                  mma_bf16(acc[h][j], lo[c][0], lo[c][1], lo[c][2], lo[c][3], bv.x, bv.y);
-                  mma_bf16(acc[h][j], hi[c][0], hi[c][1], hi[c][2], hi[c][3], bv.x, bv.y);
+                  mma_bf16(acc[h][j], lo[c].x, lo[c].y, lo[c].z, lo[c].w, bv.x, bv.y);
+                  mma_bf16(acc[h][j], hi[c].x, hi[c].y, hi[c].z, hi[c].w, bv.x, bv.y);
                 }
               }
           }
@@ -646,7 +814,7 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>()) adap
             phase ^= 1u;
           }
         }
-        if (work && c0 + w0 + 8 * t4 < p.n_res) {
+        if (work && c0 + w0 < p.n_res) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (!on[i]) continue;
@@ -658,6 +826,12 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>()) adap
             *reinterpret_cast<uint4*>(orow[i] + c0) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&hd->iempty[info]));
+      if (++info == kInfos) {
+        info = 0;
+        info_phase ^= 1u;
       }
     }
   }
@@ -684,21 +858,23 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_f32_kernel(const Expa
   const float* base = static_cast<const float*>(p.base);
   float* out = static_cast<float*>(p.out);
   for (int t = blockIdx.y; t < n_tiles; t += gridDim.y) {
-    const Tile tile = p.tiles[t];
+    const int* rows = p.tiles[t].rows;
+    const TileHead tile = head_of(&p.tiles[t]);
     const bool has = tile.adapter >= 0;
     if (!has && p.in_place) continue;
     __syncthreads();
-    for (int i = threadIdx.x; i < kTileRows * p.r; i += kThreads) {
-      const int rr = i / p.r, k = i % p.r;
-      float v = 0.f;
+    const Parts parts = parts_of(t, n_tiles, p.units, p.shrink_blocks);
+    for (int i = threadIdx.x; i < kTileRows * p.r / 4; i += kThreads) {
+      const int rr = i / (p.r / 4), k = i % (p.r / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (has && rr < tile.count) {
-        const float* u = p.u + (int64_t)(tile.start + rr) * p.r + k;
-        for (int s = 0; s < p.S; ++s) v += __ldg(u + (int64_t)s * p.rows * p.r);
-        v *= p.scale[tile.adapter];
+        const float sc = p.scale[tile.adapter];
+        v = sum_parts(p.u, p.more, tile.start, parts, p.r, rr, k);
+        v = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
       }
-      su[rr][k] = v;
+      *reinterpret_cast<float4*>(&su[rr][k]) = v;
     }
-    if (threadIdx.x < tile.count) srow[threadIdx.x] = p.order[tile.start + threadIdx.x];
+    if (threadIdx.x < tile.count) srow[threadIdx.x] = rows[threadIdx.x];
     __syncthreads();
     const float* b = static_cast<const float*>(p.b) + ((int64_t)(has ? tile.adapter : 0) * p.E + tile.expert) * p.n_out * p.r;
     const int c_end = min(p.n_res, (int)((blockIdx.x + 1) * p.col_block));
@@ -746,30 +922,24 @@ int64_t tiles_guess(const AdapterShape& s) {  // a likely number of tiles, for t
   return std::max<int64_t>(1, std::min<int64_t>(s.rows, s.rows / kTileRows + pairs));
 }
 
-// Blocks that share one reduction of K inputs, and the inputs of each: enough
-// for about four blocks per SM, at least 512 inputs (64 per warp) each
-void split(const AdapterShape& s, int K, int* S, int* k_block) {
-  const int64_t want = (4 * 148 + tiles_guess(s) - 1) / tiles_guess(s);
-  const int most = (K + 511) / 512;
-  const int n = (int)std::max<int64_t>(1, std::min<int64_t>(want, most));
-  *k_block = ((K + n - 1) / n + 63) / 64 * 64;
-  *S = (K + *k_block - 1) / *k_block;
+// Blocks of the shrink: what the registers let be resident.  The plan's size
+// does not depend on the device.
+constexpr int kMaxShrinkBlocks = 512;
+int shrink_blocks(const AdapterShape& s) {
+  return std::min(kMaxShrinkBlocks, device_sm_count() * (s.bf16 && s.r > 64 ? 1 : 2));
 }
 
 constexpr size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct PlanLayout {
-  size_t order, tiles, u, total;
+  size_t tiles, u, more, total;
 };
 PlanLayout layout(const AdapterShape& s) {
-  int s1, s2, kb;
-  split(s, s.d, &s1, &kb);
-  split(s, s.f, &s2, &kb);
   PlanLayout l;
-  l.order = kAdapterHeader;  // status word, number of tiles
-  l.tiles = l.order + up256(sizeof(int32_t) * (size_t)s.rows);
+  l.tiles = kAdapterHeader;  // status word, number of tiles
   l.u = l.tiles + up256(sizeof(Tile) * (size_t)s.rows);
-  l.total = l.u + up256(sizeof(float) * (size_t)std::max(s1, s2) * (size_t)s.rows * s.r);
+  l.more = l.u + up256(sizeof(float) * (size_t)s.rows * s.r);
+  l.total = l.more + up256(sizeof(float) * (size_t)kMaxShrinkBlocks * kTileRows * s.r);
   return l;
 }
 
@@ -802,13 +972,14 @@ cudaError_t run_expand(const ExpandParams& params, cudaStream_t stream) {
   using Sh = ExpandShape<EPI>;
   ExpandParams p = params;
   p.stage_bytes = Sh::stage_bytes(p.r);
+  constexpr int kFixed = kExpandHead + kInfos * (int)sizeof(TileInfo<RK>) + Sh::kBase;
   int per_sm = expand_blocks<RK, EPI>(), room = 0;
   for (;; --per_sm) {
-    room = 227 * 1024 / per_sm - 1024 - kExpandHead - Sh::kBase;
+    room = 227 * 1024 / per_sm - (per_sm > 1 ? 1024 : 0) - kFixed;
     if (per_sm == 1 || room >= 2 * p.stage_bytes) break;
   }
   p.stages = std::min(kMaxStages, room / p.stage_bytes);
-  const int smem = kExpandHead + Sh::kBase + p.stages * p.stage_bytes;
+  const int smem = kFixed + p.stages * p.stage_bytes;
   const cudaError_t e = allow_smem(adapter_expand_kernel<RK, EPI>, smem);
   if (e != cudaSuccess) return e;
   const int64_t most = p.rows * ((p.n_res + Sh::CW - 1) / Sh::CW);  // rounds, if every row were a tile
@@ -842,13 +1013,14 @@ cudaError_t launch_adapter_plan(const AdapterShape& s, const int32_t* offsets, c
   uint8_t* base = static_cast<uint8_t*>(plan);
   const PlanLayout l = layout(s);
   if (s.rows == 0) return cudaSuccess;
-  PlanParams p{offsets, perm, token_adapter, s.rows, s.E, s.k, s.N,
-               reinterpret_cast<int32_t*>(base + l.order), reinterpret_cast<Tile*>(base + l.tiles),
-               reinterpret_cast<int*>(base + kAdapterTilesAt), status};
   const unsigned blocks = (unsigned)((s.rows + kChunkRows - 1) / kChunkRows);
+  PlanParams p{offsets, perm, token_adapter, s.rows, s.E, s.k, s.N, reinterpret_cast<Tile*>(base + l.tiles),
+               reinterpret_cast<int*>(base + kAdapterTilesAt), status, blocks == 1 && status == plan};
   return launch_maybe_chained(adapter_plan_kernel, dim3(blocks), dim3(kPlanThreads), sizeof(int) * (size_t)(s.E + 1),
                               stream, chained, p);
 }
+
+bool adapter_plan_needs_clear(const AdapterShape& s) { return s.rows > kChunkRows; }
 
 cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, bool chained, cudaStream_t stream) {
   if (s.rows == 0) return cudaSuccess;
@@ -857,25 +1029,22 @@ cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, b
   const int K = a.gate_up ? s.d : s.f;
   const int n_res = a.gate_up ? s.f : s.d;
   const int n_out = a.gate_up && s.act == kEpiSwiGLU ? 2 * s.f : n_res;
-  const int32_t* order = reinterpret_cast<const int32_t*>(base + l.order);
   const Tile* tiles = reinterpret_cast<const Tile*>(base + l.tiles);
   const int* n_tiles = reinterpret_cast<const int*>(base + kAdapterTilesAt);
   float* u = reinterpret_cast<float*>(base + l.u);
-  int S, k_block;
-  split(s, K, &S, &k_block);
-  const int64_t guess = tiles_guess(s);
-  const unsigned tiles_grid = (unsigned)std::min<int64_t>(guess, 4096);
-  ShrinkParams sp{a.x, a.a, order, tiles, n_tiles, u, s.rows, K, s.r, s.E, k_block};
-  cudaError_t e = launch_shrink(sp, s.bf16, dim3(tiles_grid, (unsigned)S), chained, stream);
+  float* more = reinterpret_cast<float*>(base + l.more);
+  const int blocks = shrink_blocks(s), units = (K + kUnitInputs - 1) / kUnitInputs;
+  ShrinkParams sp{a.x, a.a, tiles, n_tiles, u, more, K, s.r, s.E};
+  cudaError_t e = launch_shrink(sp, s.bf16, dim3((unsigned)blocks), chained, stream);
   if (e != cudaSuccess) return e;
   // fp32: one round of the block's threads, more where there are enough tiles to fill the SMs
-  constexpr int kRound = kThreads;
-  const int64_t rounds = (n_res + kRound - 1) / kRound;
+  const int64_t guess = tiles_guess(s);
+  const int64_t rounds = (n_res + kThreads - 1) / kThreads;
   const int64_t per = std::max<int64_t>(1, std::min<int64_t>(rounds, rounds * guess / (148 * 8)));
-  const int col_block = (int)std::min<int64_t>(per, 16) * kRound;
-  ExpandParams ep{u, a.b, a.scale, a.base, a.out, order, tiles, n_tiles, s.rows, s.r, s.E, S, n_out, n_res, col_block,
-                  !a.gate_up && a.base == a.out, 0, 0, a.status, a.wait_limit_ns};
-  const dim3 grid((unsigned)((n_res + col_block - 1) / col_block), tiles_grid);
+  const int col_block = (int)std::min<int64_t>(per, 16) * kThreads;
+  ExpandParams ep{u, more, a.b, a.scale, a.base, a.out, tiles, n_tiles, s.rows, s.r, s.E, units, blocks, n_out, n_res,
+                  col_block, !a.gate_up && a.base == a.out, 0, 0, a.status, a.wait_limit_ns};
+  const dim3 grid((unsigned)((n_res + col_block - 1) / col_block), (unsigned)std::min<int64_t>(guess, 4096));
   if (!a.gate_up) return launch_expand<kEpiNone>(ep, s.bf16, grid, stream);
   return s.act == kEpiSwiGLU ? launch_expand<kEpiSwiGLU>(ep, s.bf16, grid, stream)
                              : launch_expand<kEpiGELU>(ep, s.bf16, grid, stream);

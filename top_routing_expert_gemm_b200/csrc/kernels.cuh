@@ -194,8 +194,11 @@ struct AdapterApply {
 constexpr int64_t kAdapterMaxPairs = (int64_t(1) << 23) - 3;  // experts x adapters
 constexpr size_t kAdapterTilesAt = 64;  // byte offset of the tile count in the plan's header
 size_t adapter_plan_bytes(const AdapterShape& s);
-// The plan's header (kAdapterHeader bytes) has to be zero; status: where a bad
-// adapter id is reported (the header's first word, or a workspace's).
+// The plan's header (kAdapterHeader bytes) has to be zero where
+// adapter_plan_needs_clear says so (the launch of a small batch writes it);
+// status: where a bad adapter id is reported, the header's first word (the plan
+// itself) or a workspace's.
+bool adapter_plan_needs_clear(const AdapterShape& s);
 constexpr size_t kAdapterHeader = 256;
 cudaError_t launch_adapter_plan(const AdapterShape& s, const int32_t* offsets, const int32_t* perm,
                                 const int32_t* token_adapter, void* plan, int* status, bool chained,

@@ -640,7 +640,7 @@ moe_status moe_adapter_plan(const moe_config* cfg, const moe_adapter_config* ad,
     return MOE_ERR_INVALID_ARG;
   DeviceGuard g;
   if ((st = enter(g, plan, stream)) != MOE_OK) return st;
-  MOE_CUDA_TRY(cudaMemsetAsync(plan, 0, kAdapterHeader, stream));
+  if (s.rows == 0 || adapter_plan_needs_clear(s)) MOE_CUDA_TRY(cudaMemsetAsync(plan, 0, kAdapterHeader, stream));
   MOE_CUDA_TRY(launch_adapter_plan(s, offsets, perm, token_adapter, plan, static_cast<int*>(plan), false, stream));
   return MOE_OK;
 }
@@ -698,8 +698,10 @@ moe_status moe_forward_routed(const moe_config* cfg, const moe_route_config* rou
   // everything that has to be zero is cleared ahead of the chain of launches (pdl.cuh)
   MOE_CUDA_TRY(cudaMemsetAsync(k.status, 0, 16, stream));
   if (k.counters) MOE_CUDA_TRY(cudaMemsetAsync(k.counters, 0, sizeof(int) * (size_t)k.counter_cap, stream));
-  if (rk.plan) MOE_CUDA_TRY(cudaMemsetAsync(rk.plan, 0, kAdapterHeader, stream));
-  if (rk.plan_s) MOE_CUDA_TRY(cudaMemsetAsync(rk.plan_s, 0, kAdapterHeader, stream));
+  if (rk.plan && adapter_plan_needs_clear(adapter_shape(cfg, adapters->n_adapters, adapters->rank, false)))
+    MOE_CUDA_TRY(cudaMemsetAsync(rk.plan, 0, kAdapterHeader, stream));
+  if (rk.plan_s && adapter_plan_needs_clear(adapter_shape(cfg, adapters->n_adapters, adapters->rank, true)))
+    MOE_CUDA_TRY(cudaMemsetAsync(rk.plan_s, 0, kAdapterHeader, stream));
   int32_t* ids = opt_topk_ids ? opt_topk_ids : k.ids;
   float* w = opt_topk_w ? opt_topk_w : k.w;
   int32_t* counts = opt_counts ? opt_counts : k.counts;
