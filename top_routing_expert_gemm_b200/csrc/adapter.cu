@@ -495,16 +495,36 @@ __device__ __forceinline__ float finish(float v, float up) {
 // argument's rounding (|z| 2^-24 of the exponential) are lost under half a bf16
 // step, 2^-9.  With expf and the IEEE division the kernel was issue bound.
 // Denormals are flushed: the results there are below 2^-119.
-__device__ __forceinline__ float silu_fast(float z) {
-  float e, q;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
-  return z * q;
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {  // two products in one instruction
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 silu_fast2(float2 z) {
+  float2 e = mul2(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+  e = add2(e, make_float2(1.0f, 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+  return mul2(z, e);
 }
 
+// two results of one row, rounded to bf16
 template <int EPI>
-__device__ __forceinline__ float finish_bf16(float v, float up) {
-  return EPI == kEpiSwiGLU ? silu_fast(v) * up : EPI == kEpiGELU ? gelu_f(v) : v;
+__device__ __forceinline__ uint32_t finish_bf16(float2 v, float2 up) {
+  if (EPI == kEpiSwiGLU) v = mul2(silu_fast2(v), up);
+  if (EPI == kEpiGELU) v = make_float2(gelu_f(v.x), gelu_f(v.y));
+  return pack_bf16x2(v.x, v.y);
 }
 
 // The work is a list of rounds: a tile times CW result columns (and, for
@@ -549,7 +569,7 @@ template <int EPI>
 struct ExpandShape {
   static constexpr int H = EPI == kEpiSwiGLU ? 2 : 1;
   static constexpr int CW = 32 * kWarps;        // result columns of a round
-  static constexpr int kAhead = 4;              // rounds of base in flight per warp, the current one included
+  static constexpr int kAhead = H == 2 ? 2 : 4;  // rounds of base in flight per warp, the current one included
   static constexpr int kSlot = 2 * H * 512;     // a warp's part of base
   static constexpr int kBase = kWarps * kAhead * kSlot;
   static int stage_bytes(int r) { return H * CW * r * 2; }
@@ -763,7 +783,7 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
         while (ahead < Sh::kAhead && !f_over && fetch()) {
         }
         // this round's copies are the oldest of `ahead` groups
-        static_assert(Sh::kAhead == 4, "one wait per depth");
+        static_assert(Sh::kAhead <= 4, "one wait per depth");
         if (ahead == 4) copies_wait<3>();
         else if (ahead == 3) copies_wait<2>();
         else if (ahead == 2) copies_wait<1>();
@@ -821,8 +841,8 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              o[j] = pack_bf16x2(finish_bf16<EPI>(acc[0][j][2 * i], acc[H - 1][j][2 * i]),
-                                 finish_bf16<EPI>(acc[0][j][2 * i + 1], acc[H - 1][j][2 * i + 1]));
+              o[j] = finish_bf16<EPI>(make_float2(acc[0][j][2 * i], acc[0][j][2 * i + 1]),
+                                      make_float2(acc[H - 1][j][2 * i], acc[H - 1][j][2 * i + 1]));
             *reinterpret_cast<uint4*>(orow[i] + c0) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
