@@ -239,6 +239,41 @@ def test_adapters_on_a_side_stream_and_captured():
     assert np.all(np.abs(_f64(out) - h) <= (2.0 ** -8 + 40 * U) * np.abs(h) + 1e-37)
 
 
+def test_shortest_wait_limit_is_right_or_reported_and_the_next_call_runs():
+    """With a limit of 1 ns a wait of the expand that its first try does not end
+    (a try may last until the data is there) expires: the call is right, or the
+    plan's status word says that it is not; it ends either way, and the call
+    after it (a new plan, the usual limit) is right."""
+    c = Case(T=200, d=1024, f=2048, E=4, k=2, N=3, r=64, dtype="bf16").tensors("gate_up")
+    usual = c.cfg.wait_limit_ns
+    c.cfg.wait_limit_ns = 1
+    plan = c.plan()
+    c.call("gate_up", plan)
+    st = moe.moe_device_status(plan)
+    assert st in (0, moe.MOE_ERR_TIMEOUT)
+    if st == 0:
+        c.check("gate_up")
+    c.cfg.wait_limit_ns = usual
+    c.out.fill_(5.5)
+    plan = c.plan()
+    c.call("gate_up", plan)
+    assert moe.moe_device_status(plan) == 0
+    c.check("gate_up")
+
+
+def test_plan_of_a_batch_with_long_runs_and_single_rows():
+    """Chunks of the plan that end inside runs, tiles that end inside chunks: 700
+    rows of one adapter, then every row another, then none."""
+    c = Case(T=1100, d=64, f=64, E=1, k=1, N=300, r=8, dtype="bf16", shared=True)
+    ta = np.concatenate([np.zeros(700), np.arange(300), np.full(100, -1)]).astype(np.int64)
+    c.ta, c.adapter = torch.from_numpy(ta.astype(np.int32)).cuda(), ta
+    c.tensors("down")
+    plan = c.plan()
+    c.call("down", plan)
+    assert moe.moe_device_status(plan) == 0
+    c.check("down")
+
+
 # ------------------------------------------------------------------ the layer
 def _layer(T, d, f, E, k, dtype, n_shared=0, act="swiglu", seed=0, e4m3=False, cap=0.0):
     gen = torch.Generator().manual_seed(seed)

@@ -68,8 +68,11 @@ def _check(l, bias, cfg, score, ids, w, dtype):
     want_ids, want_w, gap = oracle.route_logits(_f64(l), None if bias is None else _f64(bias), cfg.top_k, score,
                                                 cfg.n_groups, cfg.topk_groups, cfg.group_top, bool(cfg.renormalise),
                                                 float(cfg.weight_scale), dtype)
-    sure = (gap > 1e-13) | (gap == 0.0)  # binary64 sums of two scores: a few 2^-53
-    assert sure.mean() > 0.99
+    # binary64 sums of two scores are off by a few 2^-53.  Of 512 choices within
+    # 6e-8 (the closest case) the 8 first gaps are about 1.2e-10 each: one falls
+    # below 1e-13 in 0.7% of the rows.
+    sure = (gap > 1e-13) | (gap == 0.0)
+    assert sure.mean() > 0.95
     got = ids.cpu().numpy()
     assert np.array_equal(got[sure], want_ids[sure])
     gw = _f64(w)
@@ -136,11 +139,12 @@ def test_route_of_many_rows_matches_the_oracle(score, E, k, G, Gk, gtop, dtype, 
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E", [64, 512])
 @pytest.mark.parametrize("G,Gk,gtop", [(1, 1, 1), (8, 3, 2), (8, 3, 1)])
-def test_choices_closer_than_fp32_are_decided_as_the_logits_say(score, G, Gk, gtop):
+def test_choices_closer_than_fp32_are_decided_as_the_logits_say(score, G, Gk, gtop, E):
     """A bias that cancels the scores to within half an fp32 step: every order
     hangs on bits that fp32 scores do not have."""
-    T, E, k = 96, 64, 8
+    T, k = 96, 8
     rng = np.random.default_rng(9)
     base = rng.standard_normal(E).astype(np.float32)
     l = np.repeat(base[None], T, 0)

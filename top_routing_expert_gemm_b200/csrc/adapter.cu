@@ -780,8 +780,8 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
         lo[c] = has ? ti.lo[c][lane] : make_uint4(0, 0, 0, 0);
       }
       for (int q = head.x; q < head.y; ++q) {
-        while (ahead < Sh::kAhead && !f_over && fetch()) {
-        }
+        if (ahead < Sh::kAhead && !f_over) fetch();
+        if (ahead < Sh::kAhead && !f_over) fetch();  // until it is as far ahead as it may be
         // this round's copies are the oldest of `ahead` groups
         static_assert(Sh::kAhead <= 4, "one wait per depth");
         if (ahead == 4) copies_wait<3>();

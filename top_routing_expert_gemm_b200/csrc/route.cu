@@ -737,8 +737,14 @@ __global__ void __launch_bounds__(kThreads) route_tile_kernel(const __grid_const
         z *= exp_near(m - top);
         m = top;
       }
+      // a block's terms in a tree: few roundings, whatever the number of experts
 #pragma unroll
-      for (int j = 0; j < 16; ++j) z += v[j] > -INFINITY ? exp_near(v[j] - m) : 0.f;
+      for (int j = 0; j < 16; ++j) v[j] = v[j] > -INFINITY ? exp_near(v[j] - m) : 0.f;
+#pragma unroll
+      for (int half = 8; half > 0; half >>= 1)
+#pragma unroll
+        for (int j = 0; j < half; ++j) v[j] += v[j + half];
+      z += v[0];
     }
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
@@ -749,7 +755,8 @@ __global__ void __launch_bounds__(kThreads) route_tile_kernel(const __grid_const
     }
     inv = 1.0f / z;
   }
-  // the bounds of route_topk_kernel
+  // the bounds of route_topk_kernel (the denominator here: up to 8 rescalings
+  // of 2^-21.5 and 15 additions, together below 2^-18)
   const float eps = by_logit    ? 0.f
                     : p.sigmoid ? 0x1p-22f * (2.75f + bmax)
                                 : 0x1p-17f * inv + 0x1p-22f * (bmax + 1.0f * inv);
