@@ -372,16 +372,32 @@ __device__ __noinline__ int pick_near(const RouteArgs& p, const T* row, int lane
   int n = 0;
   double z = 0.0;
 #pragma unroll 1
-  for (int c0 = 0; c0 < p.E; c0 += 32) {
-    const int c = c0 + lane;
-    const float l = c < p.E ? usable<T>(Elem<T>::to_f(row[c])) : -INFINITY;
-    if (!p.sigmoid && l > -INFINITY) z += exp((double)l - (double)m);
-    const float v = (p.sigmoid ? sigmoid_fast(l) : __expf(l - m) * inv) + (p.bias && c < p.E ? p.bias[c] : 0.f);
-    const bool in = l > -INFINITY && v >= thr && (p.G == 1 || kept >> (c / gs) & 1u);
-    const unsigned who = __ballot_sync(kFull, in);
-    const int at = n + __popc(who & ((1u << lane) - 1u));
-    if (in && at < 32) cand->col[at] = c;
-    n += __popc(who);
+  for (int c0 = 0; c0 < p.E; c0 += 256) {  // 256 columns' loads in flight: the row is in L2 at best
+    float l[8], b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + 32 * j + lane;
+      l[j] = c < p.E ? usable<T>(Elem<T>::to_f(row[c])) : -INFINITY;
+      b[j] = p.bias && c < p.E ? p.bias[c] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + 32 * j + lane;
+      const float v = (p.sigmoid ? sigmoid_fast(l[j]) : __expf(l[j] - m) * inv) + b[j];
+      const bool in = l[j] > -INFINITY && v >= thr && (p.G == 1 || kept >> (c / gs) & 1u);
+      const unsigned who = __ballot_sync(kFull, in);
+      const int at = n + __popc(who & ((1u << lane) - 1u));
+      if (in && at < 32) cand->col[at] = c;
+      n += __popc(who);
+    }
+    if (!p.sigmoid) {
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j)
+        if (c0 + 32 * j + lane < p.E) {
+          const float lj = usable<T>(Elem<T>::to_f(row[c0 + 32 * j + lane]));
+          if (lj > -INFINITY) z += exp((double)lj - (double)m);
+        }
+    }
   }
   if (n > 32) return n;
   z = warp_sum(z);
