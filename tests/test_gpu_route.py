@@ -200,6 +200,25 @@ def test_extreme_logits_and_biases():
     assert torch.allclose(w, torch.tensor([[1 / 3, 1 / 3, 1 / 3, 0.0]], device="cuda").expand(2, 4))
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("b,G,want", [
+    # sums of a group's two best that pass fp32's range: 5e38 < 6e38 < inf
+    ([2e38, 3e38, 3e38, 3e38, float("inf"), 0.0, 0.0, 0.0], 4, [4, 2, 3, 5]),
+    ([2e38, 3e38, 0.0, 3e38, 3e38, 0.0, float("inf"), 0.0, 0.0], 3, [6, 3, 4, 5]),
+    # an infinite bias beside excluded experts and equal choices: the fifth slot stays empty
+    ([float("inf"), -float("inf"), float("inf"), 0.25, 0.25, float("nan"), -float("inf"), -float("inf")], 1,
+     [0, 2, 3, 4, -1]),
+])
+def test_biases_past_the_range_of_fp32(score, b, G, want):
+    bias = torch.tensor(b, device="cuda")
+    for T in (1, 33, 8201):
+        l = torch.zeros(T, len(b), device="cuda")
+        ids, w = _run(l, bias, _cfg(l, len(want), score, G, min(G, 2), 2 if G > 1 else 1))
+        assert torch.equal(ids.cpu(), torch.tensor(want, dtype=torch.int32).expand(T, -1))
+        share = torch.tensor([1.0 if i >= 0 else 0.0 for i in want])
+        assert torch.allclose(w.cpu(), (share / share.sum()).expand(T, -1))
+
+
 def test_rows_past_32_bit_offsets():
     """Row strides that take the last rows past 2^32 bytes and 2^31 elements."""
     T, E, stride = 2100, 16, 1 << 20

@@ -193,7 +193,7 @@ __device__ __noinline__ int pick_any(F (&c)[NC], const RouteArgs& p, int lane, F
       lo = fmin(lo, __shfl_xor_sync(kFull, lo, off));
       hi = fmax(hi, __shfl_xor_sync(kFull, hi, off));
     }
-    close = hi > neg_inf<F>() && lo - hi < 2 * eps;
+    close = hi > neg_inf<F>() && !(lo - hi >= 2 * eps);  // or both infinite
 #pragma unroll
     for (int j = 0; j < NC; ++j)
       if (c0 + j < p.E && !(kept >> ((c0 + j) / gs) & 1u)) c[j] = neg_inf<F>();
@@ -384,7 +384,7 @@ __device__ __noinline__ int pick_near(const RouteArgs& p, const T* row, int lane
     for (int j = 0; j < 8; ++j) {
       const int c = c0 + 32 * j + lane;
       const float v = (p.sigmoid ? sigmoid_fast(l[j]) : __expf(l[j] - m) * inv) + b[j];
-      const bool in = l[j] > -INFINITY && v >= thr && (p.G == 1 || kept >> (c / gs) & 1u);
+      const bool in = l[j] > -INFINITY && v > -INFINITY && v >= thr && (p.G == 1 || kept >> (c / gs) & 1u);
       const unsigned who = __ballot_sync(kFull, in);
       const int at = n + __popc(who & ((1u << lane) - 1u));
       if (in && at < 32) cand->col[at] = c;
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const __grid_const
         const bool kept = c0 < p.E && rank < p.Gk;
         const uint32_t lo = __reduce_min_sync(kFull, kept ? gk : 0xffffffffu);
         const uint32_t hi = __reduce_max_sync(kFull, kept ? 0u : gk);
-        near_group = hi && float_of(lo) - float_of(hi) < 2.0f * eps;
+        near_group = hi && !(float_of(lo) - float_of(hi) >= 2.0f * eps);  // or both infinite
         groups = __reduce_or_sync(kFull, kept ? 1u << mine : 0u);
         if (!kept) {
 #pragma unroll
@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(kThreads) route_tile_kernel(const __grid_const
     kept |= __shfl_xor_sync(kFull, kept, 2);
     lo = -quad_max(-lo);
     hi = quad_max(hi);
-    near_group = hi > -INFINITY && lo - hi < 2.0f * eps;
+    near_group = hi > -INFINITY && !(lo - hi >= 2.0f * eps);  // or both infinite
 #pragma unroll
     for (int i = 0; i < NB; ++i)
       if (q + 4 * i < sh.nb && !(kept >> ((q + 4 * i) / sh.nbg) & 1u)) top[i] = -INFINITY;
@@ -1117,11 +1117,14 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks<NC>) route_backward_
 
 // From this many rows (and up to 512 experts) four threads per row instead of a
 // warp: fewer instructions, a longer chain.  Measured, us, warp / four threads:
-//   rows    256 fp32, sigmoid in groups, k 8   128 bf16, softmax, k 4   8 fp32, k 2
-//   1024    8.2 / 13.7                         3.7 / 4.8                3.3 / 3.7
-//   4096    13.8 / 16.7                        4.9 / 4.9                4.0 / 3.6
-//   8192    19.8 / 18.9                        8.9 / 6.3                6.6 / 3.8
-//   65536   102 / 55                           54 / 16.5                42 / 11.4
+//   rows    256 fp32,            512 bf16,        128 bf16,      8 fp32,
+//           sigmoid in groups,   sigmoid, bias,   softmax, k 4   softmax, k 2
+//           bias, k 8            k 16
+//   16      4.1 / 8.3            5.4 / 15.1       3.2 / 4.4      2.9 / 3.4
+//   1024    5.8 / 10.2           10.4 / 20.6      3.5 / 4.7      3.2 / 3.6
+//   4096    11.5 / 13.9          19.8 / 25.5      6.3 / 4.9      3.9 / 3.7
+//   8192    18.0 / 17.0          30.0 / 28.0      9.9 / 6.3      6.6 / 3.9
+//   65536   97 / 51              156 / 148        52 / 16.3      41 / 11.2
 constexpr int64_t kTileMinRows = 8192;
 
 // Blocks: a warp per row up to a few resident blocks per SM, then rows in turn
