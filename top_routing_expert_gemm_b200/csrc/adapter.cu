@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
         ok = tc::mbar_wait_bounded(tc::smem_u32(&hd->iempty[info]), info_phase ^ 1u, abort_flag, p.wait_limit_ns,
                                    p.status);
       if (!__shfl_sync(kFull, ok, 0)) break;
+      __syncwarp();  // what lane 0 has seen holds for the warp
       TileInfo<RK>& to = infos[info];
       if (lane == 0) *reinterpret_cast<int4*>(&to) = make_int4(q0, q_end, tile.count, has);
       if (lane < kTileRows) to.rows[lane] = row;
@@ -724,6 +725,7 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
       if (f_q == f_end) {
         const int known = lane == 0 ? (int)tc::mbar_try_wait(tc::smem_u32(&hd->ifull[f_info]), f_phase) : 0;
         if (!__shfl_sync(kFull, known, 0)) return false;
+        __syncwarp();  // what lane 0 has seen holds for the warp
         const TileInfo<RK>& ti = infos[f_info];
         if (ti.count < 0) {
           f_over = true;

@@ -269,7 +269,7 @@ moe_status adapter_apply(const moe_config* cfg, const moe_adapter_config* ad, bo
   if ((st = enter(g, plan, stream)) != MOE_OK) return st;
   if ((st = g.same_device(out)) != MOE_OK) return st;
   MOE_CUDA_TRY(launch_adapter_apply(s, AdapterApply{gate_up, x, a, b, scale, base, out, plan, static_cast<int*>(plan),
-                                                   wait_limit(cfg)}, false, stream));
+                                                   wait_limit(cfg)}, true, stream));
   return MOE_OK;
 }
 
@@ -641,7 +641,7 @@ moe_status moe_adapter_plan(const moe_config* cfg, const moe_adapter_config* ad,
   DeviceGuard g;
   if ((st = enter(g, plan, stream)) != MOE_OK) return st;
   if (s.rows == 0 || adapter_plan_needs_clear(s)) MOE_CUDA_TRY(cudaMemsetAsync(plan, 0, kAdapterHeader, stream));
-  MOE_CUDA_TRY(launch_adapter_plan(s, offsets, perm, token_adapter, plan, static_cast<int*>(plan), false, stream));
+  MOE_CUDA_TRY(launch_adapter_plan(s, offsets, perm, token_adapter, plan, static_cast<int*>(plan), true, stream));
   return MOE_OK;
 }
 
