@@ -91,6 +91,8 @@ class Case:
 
     def plan(self, stream=None):
         p = torch.full((moe.moe_adapter_plan_bytes(self.cfg, self.ad),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN wherever nothing is written
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())  # the fill above
         moe.moe_adapter_plan(self.cfg, self.ad, self.offsets, self.perm, self.ta, p, stream=stream)
         return p
 
@@ -237,6 +239,43 @@ def test_adapters_on_a_side_stream_and_captured():
     pre = _f64(c.base)
     h = oracle.silu(pre[:, :f]) * pre[:, f:]
     assert np.all(np.abs(_f64(out) - h) <= (2.0 ** -8 + 40 * U) * np.abs(h) + 1e-37)
+
+
+def test_calls_in_a_row_and_on_two_streams():
+    """Plans, first and second projections one after the other with nothing
+    between them, over two batches of different sizes, each on a stream of its
+    own at the same time: as the same calls made alone."""
+    cases = [Case(T=T, d=256, f=264, E=4, k=2, N=6, r=16, dtype="bf16", seed=T) for T in (40, 700)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    alone, plans = [], []
+    for c in cases:
+        c.tensors("gate_up")
+        c.down = Case.__new__(Case)
+        c.down.__dict__.update(c.__dict__)
+        c.down.tensors("down")
+        plan = c.plan()
+        c.call("gate_up", plan)
+        c.down.call("down", plan)
+        alone.append((c.out.clone(), c.down.out.clone()))
+        plans.append(plan)
+    none = [torch.full_like(c.ta, -1) for c in cases]
+    got = []
+    torch.cuda.synchronize()
+    for i in range(20):
+        for c, plan, s, other in zip(cases, plans, streams, none):
+            with torch.cuda.stream(s):
+                c.out.fill_(5.5)
+                c.down.out.fill_(5.5)
+                # a plan that the next one replaces at once, and a call on it
+                moe.moe_adapter_plan(c.cfg, c.ad, c.offsets, c.perm, other, plan)
+                c.call("gate_up", plan)
+                moe.moe_adapter_plan(c.cfg, c.ad, c.offsets, c.perm, c.ta, plan)
+                c.down.call("down", plan)
+                c.call("gate_up", plan)
+                got.append((c.out.clone(), c.down.out.clone()))
+    torch.cuda.synchronize()
+    for i, (h, y) in enumerate(got):
+        assert torch.equal(h, alone[i % 2][0]) and torch.equal(y, alone[i % 2][1])
 
 
 def test_shortest_wait_limit_is_right_or_reported_and_the_next_call_runs():

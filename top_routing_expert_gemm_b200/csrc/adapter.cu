@@ -284,68 +284,93 @@ template <int RT>
 constexpr int shrink_stage() { return 2 * (2 + RT) * 512; }
 template <int RT>
 constexpr int shrink_smem() {
-  const int ring = kWarps * ring_stages(shrink_stage<RT>()) * shrink_stage<RT>();
-  const int red = kWarps / 2 * 16 * RT * 8 * 4;  // the fold of the warps' sums, over the drained rings
-  return ring > red ? ring : red;
+  return kWarps * (ring_stages(shrink_stage<RT>()) * shrink_stage<RT>() + RT * 512);  // the rings and the warps' sums
 }
 template <int RT>
 __global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) adapter_shrink_kernel(const ShrinkParams p) {
   constexpr int kStage = shrink_stage<RT>(), kStages = ring_stages(kStage);
   extern __shared__ __align__(16) uint8_t smem[];
-  float(*red)[16 * RT * 8] = reinterpret_cast<float(*)[16 * RT * 8]>(smem);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int g = lane / 4, t4 = lane % 4;
   uint8_t* ring_ptr = smem + warp * (kStages * kStage) + lane * 16;
   const uint32_t ring = tc::smem_u32(ring_ptr);
+  float4* sums = reinterpret_cast<float4*>(smem + kWarps * kStages * kStage);  // [warps][RT][32]
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
   const int units = (p.K + kUnitInputs - 1) / kUnitInputs;
   const Run run = run_of((int64_t)*p.n_tiles * units, blockIdx.x, gridDim.x);
-  for (int64_t at = run.lo; at < run.hi;) {
+
+  // a piece of the run is a tile's units, or what the run has of them.  The one
+  // that starts at `at` is looked at while the one before it is computed:
+  int64_t at = run.lo;
+  TileHead next;
+  int next_row[2], next_lo = 0, next_hi = 0;
+  auto look = [&] {
     const int t = (int)quotient(at, units);
-    const int* rows = p.tiles[t].rows;
-    const TileHead tile = head_of(&p.tiles[t]);
-    const int u_lo = (int)(at - (int64_t)t * units), u_hi = (int)min((int64_t)units, u_lo + (run.hi - at));
-    at += u_hi - u_lo;
-    if (tile.adapter < 0) continue;
-    const int k_lo = u_lo * kUnitInputs, k_hi = min(p.K, u_hi * kUnitInputs);
-    const __nv_bfloat16* a =
-        static_cast<const __nv_bfloat16*>(p.a) + ((int64_t)tile.adapter * p.E + tile.expert) * p.r * p.K;
-    int64_t row[2];
+    next = head_of(&p.tiles[t]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) row[h] = h * 8 + g < tile.count ? rows[h * 8 + g] : -1;
+    for (int h = 0; h < 2; ++h) next_row[h] = p.tiles[t].rows[h * 8 + g];
+    next_lo = (int)(at - (int64_t)t * units);
+    next_hi = (int)min((int64_t)units, next_lo + (run.hi - at));
+    at += next_hi - next_lo;
+  };
+  const __nv_bfloat16* a = nullptr;
+  int count = 0, row[2], k_first = 0, k_hi = 0, slot = 0;
+  float* u = nullptr;  // where the piece's sums go
+  auto issue = [&](int k0, int to) {
+    const uint32_t dst = ring + to * kStage;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int k = k0 + 32 * c + 8 * t4;
+      const bool in = k < k_hi;  // K is a multiple of 8
+#pragma unroll
+      for (int n = 0; n < RT; ++n) {
+        const bool on = in && n * 8 + g < p.r;
+        copy16(dst + (c * RT + n) * 512, on ? a + (int64_t)(n * 8 + g) * p.K + k : a, on);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool on = in && h * 8 + g < count;
+        copy16(dst + (2 * RT + c * 2 + h) * 512, on ? x + (int64_t)row[h] * p.K + k : x, on);
+      }
+    }
+  };
+  // the first copies of the piece that was looked at
+  auto begin = [&] {
+    count = next.count;
+    row[0] = next_row[0];
+    row[1] = next_row[1];
+    a = static_cast<const __nv_bfloat16*>(p.a) + ((int64_t)next.adapter * p.E + next.expert) * p.r * p.K;
+    u = next_lo == 0 ? p.u + (int64_t)next.start * p.r : p.more + (int64_t)blockIdx.x * kTileRows * p.r;
+    k_hi = min(p.K, next_hi * kUnitInputs);
+    k_first = next_lo * kUnitInputs + warp * kUnit;
+#pragma unroll
+    for (int d = 0; d < kStages - 1; ++d) {
+      if (k_first + d * kWarps * kUnit < k_hi) issue(k_first + d * kWarps * kUnit, slot + d < kStages ? slot + d : slot + d - kStages);
+      copies_commit();
+    }
+  };
+  // the next piece with an adapter, from what is looked at; false at the run's end
+  auto settle = [&](bool any) {
+    while (any && next.adapter < 0) {
+      any = at < run.hi;
+      if (any) look();
+    }
+    return any;
+  };
+  bool any = at < run.hi;
+  if (any) look();
+  any = settle(any);
+  if (any) begin();
+  while (any) {
+    any = at < run.hi;
+    if (any) look();
     float acc[RT][4];
 #pragma unroll
     for (int n = 0; n < RT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-
-    auto issue = [&](int k0, int slot) {
-      const uint32_t dst = ring + slot * kStage;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int k = k0 + 32 * c + 8 * t4;
-        const bool in = k < k_hi;  // K is a multiple of 8
-#pragma unroll
-        for (int n = 0; n < RT; ++n) {
-          const bool on = in && n * 8 + g < p.r;
-          copy16(dst + (c * RT + n) * 512, on ? a + (int64_t)(n * 8 + g) * p.K + k : a, on);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool on = in && row[h] >= 0;
-          copy16(dst + (2 * RT + c * 2 + h) * 512, on ? x + row[h] * p.K + k : x, on);
-        }
-      }
-    };
-    const int k_first = k_lo + warp * kUnit;
-#pragma unroll
-    for (int d = 0; d < kStages - 1; ++d) {
-      if (k_first + d * kWarps * kUnit < k_hi) issue(k_first + d * kWarps * kUnit, d);
-      copies_commit();
-    }
-    int slot = 0;
     for (int k0 = k_first; k0 < k_hi; k0 += kWarps * kUnit) {
       const int ahead = k0 + (kStages - 1) * kWarps * kUnit;
       if (ahead < k_hi) issue(ahead, slot == 0 ? kStages - 1 : slot - 1);
@@ -364,40 +389,34 @@ __global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) adapter_shrink_kern
       }
       if (++slot == kStages) slot = 0;
     }
-    // the warps' sums: halves are folded, in a fixed order
+    // the next piece's first copies go out before the warps' sums are added up
+    const int n_rows = count;
+    float* to = u;
+    any = settle(any);
+    if (any) begin();
 #pragma unroll
-    for (int half = kWarps / 2; half > 0; half >>= 1) {
-      __syncthreads();
-      if (warp >= half && warp < 2 * half) {
+    for (int n = 0; n < RT; ++n)
+      sums[(warp * RT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < RT * 32; i += kThreads) {  // in a fixed order
+      float4 v[kWarps];
 #pragma unroll
-        for (int n = 0; n < RT; ++n)
-          *reinterpret_cast<float4*>(&red[warp - half][(n * 32 + lane) * 4]) =
-              make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-      }
-      __syncthreads();
-      if (warp < half) {
+      for (int w = 0; w < kWarps; ++w) v[w] = sums[w * RT * 32 + i];
 #pragma unroll
-        for (int n = 0; n < RT; ++n) {
-          const float4 o = *reinterpret_cast<const float4*>(&red[warp][(n * 32 + lane) * 4]);
-          acc[n][0] += o.x;
-          acc[n][1] += o.y;
-          acc[n][2] += o.z;
-          acc[n][3] += o.w;
+      for (int half = kWarps / 2; half > 0; half >>= 1)
+#pragma unroll
+        for (int w = 0; w < half; ++w) {
+          v[w].x += v[w + half].x;
+          v[w].y += v[w + half].y;
+          v[w].z += v[w + half].z;
+          v[w].w += v[w + half].w;
         }
-      }
+      const int i0 = i % 32 / 4, c = i / 32 * 8 + 2 * (i % 4);
+      if (i0 < n_rows && c < p.r) *reinterpret_cast<float2*>(to + (int64_t)i0 * p.r + c) = make_float2(v[0].x, v[0].y);
+      if (i0 + 8 < n_rows && c < p.r)
+        *reinterpret_cast<float2*>(to + (int64_t)(i0 + 8) * p.r + c) = make_float2(v[0].z, v[0].w);
     }
-    if (warp == 0) {
-      float* u = u_lo == 0 ? p.u + (int64_t)tile.start * p.r : p.more + (int64_t)blockIdx.x * kTileRows * p.r;
-#pragma unroll
-      for (int n = 0; n < RT; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = h * 8 + g, c = n * 8 + 2 * t4;
-          if (i < tile.count && c < p.r)
-            *reinterpret_cast<float2*>(u + (int64_t)i * p.r + c) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
-        }
-    }
-    __syncthreads();  // the fold is read before the next tile's copies land there
+    __syncthreads();
   }
 }
 
