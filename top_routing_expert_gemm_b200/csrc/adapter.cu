@@ -13,6 +13,11 @@
 //           blocks and the warps of each; partial sums in fp32, added in a
 //           fixed order
 //   expand  base + s B U per tile and column block, then the activation
+// Measured (plan, shrink, expand): 2048 tokens, k = 2, 4096 -> 14336, 12 requests,
+// rank 16: 6, 12, 87 us; 8192 tokens, k = 4, 2880 -> 2880, 24 requests, rank 8: 7,
+// 41, 76; 64 tokens of 64 adapters, k = 2, 14336 -> 4096, rank 16: 6, 13, 12; one
+// token, k = 2, 4096 -> 14336: 5, 4.5, 7.5.  Chained, a call takes 2 to 5 us less
+// than their sum.
 // Rows never meet: a row's result does not depend on the tile it falls into.
 //
 // Bound by bytes: base and result once, x once, the touched adapters' A and B
@@ -206,7 +211,10 @@ struct ShrinkParams {
 // tile that an earlier block began and the beginning of one that a later block
 // ends: the partial sum of a beginning goes to the tile's place in u, that of a
 // continuation (a block has one at most) to the block's place in more, and the
-// expand adds them in the order of the blocks.
+// expand adds them in the order of the blocks.  While a block computes a piece it
+// looks at the next one, and fetches its first inputs before it adds up the
+// warps' sums: 41 against 45.5 us for 32768 rows of 2880, rank 8 (189 MB of x:
+// 4.6 TB/s).
 constexpr int kUnitInputs = 64 * kWarps;
 // a / b for a >= 0: 64-bit divisions are slow, and the numbers seldom need them
 __device__ __forceinline__ int64_t quotient(int64_t a, int b) {
@@ -546,18 +554,26 @@ __device__ __forceinline__ uint32_t finish_bf16(float2 v, float2 up) {
   return pack_bf16x2(v.x, v.y);
 }
 
-// The work is a list of rounds: a tile times CW result columns (and, for
-// SwiGLU, the matching up columns), tile after tile; every block takes an equal
+// The work is a list of rounds: a tile times two groups of 256 result columns
+// (SwiGLU: one group and its up columns), tile after tile; every block takes an equal
 // run of it, so the blocks end together whatever the tiles are.  A producer warp
 // goes ahead of eight consumer warps: per tile it sums U, scales it and leaves it
 // as MMA fragments in shared memory with the tile's rows (the eight would
 // otherwise do it eight times, and wait for it), and per round it fetches the
-// columns' rows of B (one contiguous piece each) with bulk copies into a ring of
-// stages under mbarriers.  A consumer warp takes 32 columns of a round and
-// fetches its part of base itself, each lane its own 16-byte vectors, a few
-// rounds ahead and on into the next tile.  (base by bulk copies as well, a
+// columns' rows of B (one contiguous piece per group) with bulk copies into a ring of
+// stages under mbarriers.  A consumer warp takes 32 columns of each group and
+// fetches its part of base itself, each lane its own 16-byte vectors, a
+// round ahead and on into the next tile.  (base by bulk copies as well, a
 // segment of each row, measured 186 against 117 us for 16-byte copies: at 256
-// bytes a bulk copy costs more than it moves.)
+// bytes a bulk copy costs more than it moves.)  One group per round and three
+// blocks per SM instead of two took 83 against 76 us for 32768 rows of 2880, rank 8:
+// the second group hides the first one's latencies.
+//
+// Measured: 4096 rows of 14336, SwiGLU, rank 16 (352 MB of base and result): 87 us,
+// 4.1 TB/s; 32768 rows of 2880, rank 8 (377 MB): 76 us, 5.0 TB/s, of 6.5 that a copy
+// reaches.  Not memory but the issue of dependent instructions bounds it (half the
+// issue slots are used; without its activation the first takes 78 us, without
+// its MMAs 73, without base or stores 88).
 //
 // Column 2t+i of instruction j stands for column 8t + 2j + i of the warp's 32, so
 // a lane ends with 8 consecutive columns of a row: base is read and the result
@@ -586,17 +602,18 @@ constexpr int kExpandThreads = kThreads + 32;
 
 template <int EPI>
 struct ExpandShape {
-  static constexpr int H = EPI == kEpiSwiGLU ? 2 : 1;
-  static constexpr int CW = 32 * kWarps;        // result columns of a round
-  static constexpr int kAhead = H == 2 ? 2 : 4;  // rounds of base in flight per warp, the current one included
-  static constexpr int kSlot = 2 * H * 512;     // a warp's part of base
+  static constexpr int H = 2;             // column groups of a round: gate and up, or neighbours
+  static constexpr int GW = 32 * kWarps;  // columns of a group
+  static constexpr int CW = EPI == kEpiSwiGLU ? GW : H * GW;  // result columns of a round
+  static constexpr int kAhead = 2;           // rounds of base in flight per warp, the current one included
+  static constexpr int kSlot = 2 * H * 512;  // a warp's part of base
   static constexpr int kBase = kWarps * kAhead * kSlot;
-  static int stage_bytes(int r) { return H * CW * r * 2; }
+  static int stage_bytes(int r) { return H * GW * r * 2; }
 };
 
 // Blocks per SM that the registers (and, below, the rings) leave room for
 template <int RK, int EPI>
-constexpr int expand_blocks() { return RK > 2 ? 1 : RK == 1 && EPI != kEpiSwiGLU ? 3 : 2; }
+constexpr int expand_blocks() { return RK > 2 ? 1 : 2; }
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, int bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -608,7 +625,8 @@ template <int RK, int EPI>
 __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
     adapter_expand_kernel(const __grid_constant__ ExpandParams p) {
   using Sh = ExpandShape<EPI>;
-  constexpr int H = Sh::H, CW = Sh::CW;
+  constexpr int H = Sh::H, CW = Sh::CW, GW = Sh::GW;
+  constexpr bool kPair = EPI == kEpiSwiGLU;  // the groups are gate and up
   extern __shared__ __align__(16) uint8_t smem[];
   ExpandHeader* hd = reinterpret_cast<ExpandHeader*>(smem);
   TileInfo<RK>* infos = reinterpret_cast<TileInfo<RK>*>(smem + kExpandHead);
@@ -633,7 +651,8 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
   volatile int* abort_flag = &hd->abort;
-  const int b_bytes = CW * p.r * 2;
+  const int b_bytes = GW * p.r * 2;
+  const int apart = kPair ? p.n_res : GW;  // columns between the groups, in base and B
   int stage = 0, info = 0;  // stages and tiles in turn, with their parities
   uint32_t phase = 0, info_phase = 0;
 
@@ -713,11 +732,11 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
           ok = tc::mbar_wait_bounded(tc::smem_u32(&hd->empty[stage]), phase ^ 1u, abort_flag, p.wait_limit_ns,
                                      p.status);
           if (!ok) break;
-          tc::mbar_expect_tx(full, H * cols * p.r * 2);
+          tc::mbar_expect_tx(full, (kPair ? 2 : 1) * cols * p.r * 2);
           hd->fill_par[stage] = (int)phase;
           const uint32_t dst = tc::smem_u32(ring + stage * p.stage_bytes);
 #pragma unroll
-          for (int h = 0; h < H; ++h)
+          for (int h = 0; h < (kPair ? 2 : 1); ++h)
             bulk_copy(dst + h * b_bytes, b + (int64_t)(h * p.n_res + c0) * p.r, cols * p.r * 2, full);
           if (++stage == p.stages) {
             stage = 0;
@@ -757,18 +776,18 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
           f_on[i] = i * 8 + g < ti.count;
           const int64_t row = f_on[i] ? ti.rows[i * 8 + g] : 0;
 #pragma unroll
-          for (int h = 0; h < H; ++h) src[i][h] = base + row * p.n_out + h * p.n_res + f_q * CW + w0;
+          for (int h = 0; h < H; ++h) src[i][h] = base + row * p.n_out + h * apart + f_q * CW + w0;
         }
         if (++f_info == kInfos) {
           f_info = 0;
           f_phase ^= 1u;
         }
       }
-      const bool in = f_q * CW + w0 < p.n_res;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int h = 0; h < H; ++h) {
+          const bool in = f_q * CW + (kPair ? 0 : h * GW) + w0 < p.n_res;
           copy16(mine32 + f_slot * Sh::kSlot + (i * H + h) * 512, src[i][h], in && f_on[i]);
           src[i][h] += CW;
         }
@@ -810,7 +829,7 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
         else if (ahead == 2) copies_wait<1>();
         else copies_wait<0>();
         const int c0 = q * CW;
-        const bool work = c0 + warp * 32 < p.n_res;
+        const bool work = c0 + warp * 32 < p.n_res;  // else the second group has none either
         float acc[H][4][4];
         if (work) {
 #pragma unroll
@@ -855,16 +874,18 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
             phase ^= 1u;
           }
         }
-        if (work && c0 + w0 < p.n_res) {
+#pragma unroll
+        for (int h = 0; h < (kPair ? 1 : H); ++h) {
+          if (!work || c0 + h * GW + w0 >= p.n_res) break;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (!on[i]) continue;
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              o[j] = finish_bf16<EPI>(make_float2(acc[0][j][2 * i], acc[0][j][2 * i + 1]),
+              o[j] = finish_bf16<EPI>(make_float2(acc[h][j][2 * i], acc[h][j][2 * i + 1]),
                                       make_float2(acc[H - 1][j][2 * i], acc[H - 1][j][2 * i + 1]));
-            *reinterpret_cast<uint4*>(orow[i] + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(orow[i] + c0 + h * GW) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
       }
