@@ -241,6 +241,19 @@ def test_adapters_on_a_side_stream_and_captured():
     assert np.all(np.abs(_f64(out) - h) <= (2.0 ** -8 + 40 * U) * np.abs(h) + 1e-37)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_equal_calls_give_equal_results(dtype):
+    """More chunks than one of rows, and tiles whose sums several blocks share."""
+    c = Case(T=6000, d=64, f=2560, E=4, k=2, N=9, r=8, dtype=dtype).tensors("down")
+    outs = []
+    for _ in range(12):
+        c.out.fill_(5.5)
+        c.call("down", c.plan())
+        outs.append(c.out.clone())
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    c.check("down")
+
+
 def test_calls_in_a_row_and_on_two_streams():
     """Plans, first and second projections one after the other with nothing
     between them, over two batches of different sizes, each on a stream of its

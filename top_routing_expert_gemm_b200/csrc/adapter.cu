@@ -9,23 +9,23 @@
 //   plan    groups the rows of equal (expert, adapter) into tiles of up to 16
 //           rows: chunks of 256 rows are sorted inside a block, so no global
 //           sort and no histogram over the pairs is needed
-//   shrink  U = A x per tile, the reduction over the inputs split over S
+//   shrink  U = A x per tile, the reduction over the inputs split over
 //           blocks and the warps of each; partial sums in fp32, added in a
 //           fixed order
 //   expand  base + s B U per tile and column block, then the activation
 // Measured (plan, shrink, expand): 2048 tokens, k = 2, 4096 -> 14336, 12 requests,
-// rank 16: 6, 12, 87 us; 8192 tokens, k = 4, 2880 -> 2880, 24 requests, rank 8: 7,
+// rank 16: 7.5, 12, 87 us; 8192 tokens, k = 4, 2880 -> 2880, 24 requests, rank 8: 10,
 // 41, 76; 64 tokens of 64 adapters, k = 2, 14336 -> 4096, rank 16: 6, 13, 12; one
 // token, k = 2, 4096 -> 14336: 5, 4.5, 7.5.  Chained, a call takes 2 to 5 us less
 // than their sum.
-// Rows never meet: a row's result does not depend on the tile it falls into.
+// Rows never meet; of the others in its batch a row's result depends by the
+// order of U's partial sums at most, and equal calls give equal results.
 //
 // Bound by bytes: base and result once, x once, the touched adapters' A and B
 // once (a tile reads its pair's weights, tiles of one pair meet in L2).  The
 // products have a depth or width of rank, 8 to 128, so the tensor work is small
-// and mma.sync, whose operands come straight from global memory in fragment
-// order, does it without a shared-memory stage; a 128-row tcgen05 tile would
-// be mostly empty.  In fp32 layers everything is fmaf on the CUDA cores.
+// and mma.sync does it, on tiles of 16 rows; a 128-row tcgen05 tile would be
+// mostly empty.  In fp32 layers everything is fmaf on the CUDA cores.
 #include <algorithm>
 
 #include "common.cuh"
@@ -71,7 +71,10 @@ struct PlanParams {
   int E, k, N;
   Tile* tiles;
   int* n_tiles;
+  int* turn;                 // several blocks: which chunk is next,
+  unsigned long long* state; // and what is known of each (kKnown...)
   int* status;
+  uint64_t wait_limit_ns;
   bool clear;  // one block: the status word is this call's own
 };
 
@@ -80,16 +83,63 @@ struct PlanParams {
 // all keys differ and one comparison ranks stably.
 constexpr int kPlanThreads = 4 * kChunkRows;
 
+// The tiles stand in the order of the chunks, so that equal calls cut them into
+// equal runs and give equal results.  A chunk's place is the number of tiles
+// before it: every block publishes its own number, and its first warp adds up
+// those before it, 32 at a time, down to one that has published its total.
+// Blocks take their chunks in turn, so whoever waits waits for running blocks.
+// (Places from one atomic counter took 6.3 us against 7.5 for 16 chunks and 7 against
+// 10 for 128, but then the order of the tiles, and with it the last bits of U,
+// changed from call to call.)
+constexpr unsigned long long kKnownOwn = 1, kKnownTotal = 2, kGivenUp = 3;  // low bits; the number above them
+__device__ __forceinline__ int64_t tiles_before(const PlanParams& p, int64_t chunk, int64_t own, int lane) {
+  volatile unsigned long long* state = p.state;
+  if (lane == 0 && chunk > 0) state[chunk] = (unsigned long long)own << 2 | kKnownOwn;
+  int64_t before = 0;
+  bool over = chunk == 0, lost = false;
+  uint64_t t0 = 0;
+  for (int64_t last = chunk - 1; !over;) {
+    const unsigned long long v = last >= lane ? state[last - lane] : +kKnownTotal;
+    const unsigned total = __ballot_sync(kFull, (v & 3) == kKnownTotal), none = __ballot_sync(kFull, (v & 3) == 0);
+    const unsigned upto = total ? (2u << (__ffs(total) - 1)) - 1 : kFull;  // the lanes that count
+    lost = __any_sync(kFull, (v & 3) == kGivenUp);
+    if (!(none & upto) && !lost) {
+      int64_t n = upto >> lane & 1u ? (int64_t)(v >> 2) : 0;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(kFull, n, off);
+      before += n;
+      over = total != 0;
+      last -= 32;
+      continue;
+    }
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    lost = __any_sync(kFull, lost || now - t0 > p.wait_limit_ns);
+    if (lost) break;
+  }
+  if (lane == 0) {
+    if (lost) set_status(p.status, kDevTimeout);
+    state[chunk] = lost ? kGivenUp : (unsigned long long)(before + own) << 2 | kKnownTotal;
+  }
+  return lost ? -1 : before;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanParams p) {
   extern __shared__ int s_off[];  // [E+1]
   __shared__ __align__(16) int keys[kChunkRows];
   __shared__ int sorted[kChunkRows], s_row[kChunkRows];
   __shared__ int warp_sums[kChunkRows / 32];
-  __shared__ int s_base;
+  __shared__ int s_base, s_chunk;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   grid_dependency_wait();  // the dispatch (programmatic launch)
   if (tid == 0) grid_launch_dependents();
-  const int64_t row0 = (int64_t)blockIdx.x * kChunkRows;
+  int chunk = 0;
+  if (gridDim.x > 1) {
+    if (tid == 0) s_chunk = atomicAdd(p.turn, 1);
+    __syncthreads();
+    chunk = s_chunk;
+  }
+  const int64_t row0 = (int64_t)chunk * kChunkRows;
   const int64_t row = row0 + tid;
   const bool mine_to_load = tid < kChunkRows && row < p.rows;
   bool bad = false;
@@ -171,19 +221,25 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
   const unsigned heads = __ballot_sync(kFull, head);
   if (lane == 0 && tid < kChunkRows) warp_sums[warp] = __popc(heads);
   __syncthreads();
-  if (tid == 0) {
+  if (warp == 0) {
     int n = 0;
-    for (int w = 0; w < kChunkRows / 32; ++w) {
-      const int c = warp_sums[w];
-      warp_sums[w] = n;
-      n += c;
+#pragma unroll
+    for (int w = 0; w < kChunkRows / 32; ++w) n += warp_sums[w];
+    const int64_t before = gridDim.x > 1 ? tiles_before(p, chunk, n, lane) : 0;
+    __syncwarp();
+    if (lane == 0) {
+      if (chunk == (int)gridDim.x - 1) *p.n_tiles = before < 0 ? 0 : (int)before + n;  // 0: nothing is done
+      s_base = (int)before;
+      n = 0;
+      for (int w = 0; w < kChunkRows / 32; ++w) {
+        const int c = warp_sums[w];
+        warp_sums[w] = n;
+        n += c;
+      }
     }
-    s_base = 0;  // the order of the tiles changes no result
-    if (gridDim.x == 1) *p.n_tiles = n;
-    else if (n) s_base = atomicAdd(p.n_tiles, n);
   }
   __syncthreads();
-  if (mine != kSkip) {
+  if (mine != kSkip && s_base >= 0) {
     // the tile of a position: the heads up to it, less one
     Tile* tile = p.tiles + s_base + warp_sums[warp] + __popc(heads & (0xffffffffu >> (31 - lane))) - 1;
     tile->rows[place] = s_row[tid];
@@ -994,11 +1050,13 @@ int shrink_blocks(const AdapterShape& s) {
 constexpr size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct PlanLayout {
-  size_t tiles, u, more, total;
+  size_t state, tiles, u, more, total;
 };
+int64_t chunks_of(const AdapterShape& s) { return (s.rows + kChunkRows - 1) / kChunkRows; }
 PlanLayout layout(const AdapterShape& s) {
   PlanLayout l;
-  l.tiles = kAdapterHeader;  // status word, number of tiles
+  l.state = kAdapterHeader;  // behind the status word, the number of tiles and the chunks' turn
+  l.tiles = l.state + (s.rows > kChunkRows ? up256(sizeof(unsigned long long) * (size_t)chunks_of(s)) : 0);
   l.u = l.tiles + up256(sizeof(Tile) * (size_t)s.rows);
   l.more = l.u + up256(sizeof(float) * (size_t)s.rows * s.r);
   l.total = l.more + up256(sizeof(float) * (size_t)kMaxShrinkBlocks * kTileRows * s.r);
@@ -1070,19 +1128,22 @@ cudaError_t launch_expand(const ExpandParams& p, bool bf16, dim3 grid, cudaStrea
 size_t adapter_plan_bytes(const AdapterShape& s) { return layout(s).total; }
 
 cudaError_t launch_adapter_plan(const AdapterShape& s, const int32_t* offsets, const int32_t* perm,
-                                const int32_t* token_adapter, void* plan, int* status, bool chained,
-                                cudaStream_t stream) {
+                                const int32_t* token_adapter, void* plan, int* status, uint64_t wait_limit_ns,
+                                bool chained, cudaStream_t stream) {
   uint8_t* base = static_cast<uint8_t*>(plan);
   const PlanLayout l = layout(s);
   if (s.rows == 0) return cudaSuccess;
-  const unsigned blocks = (unsigned)((s.rows + kChunkRows - 1) / kChunkRows);
+  const unsigned blocks = (unsigned)chunks_of(s);
   PlanParams p{offsets, perm, token_adapter, s.rows, s.E, s.k, s.N, reinterpret_cast<Tile*>(base + l.tiles),
-               reinterpret_cast<int*>(base + kAdapterTilesAt), status, blocks == 1 && status == plan};
+               reinterpret_cast<int*>(base + kAdapterTilesAt), reinterpret_cast<int*>(base + kAdapterTurnAt),
+               reinterpret_cast<unsigned long long*>(base + l.state), status, wait_limit_ns, blocks == 1 && status == plan};
   return launch_maybe_chained(adapter_plan_kernel, dim3(blocks), dim3(kPlanThreads), sizeof(int) * (size_t)(s.E + 1),
                               stream, chained, p);
 }
 
-bool adapter_plan_needs_clear(const AdapterShape& s) { return s.rows > kChunkRows; }
+size_t adapter_plan_clear_bytes(const AdapterShape& s) {
+  return s.rows == 0 ? kAdapterHeader : s.rows > kChunkRows ? layout(s).tiles : 0;
+}
 
 cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, bool chained, cudaStream_t stream) {
   if (s.rows == 0) return cudaSuccess;

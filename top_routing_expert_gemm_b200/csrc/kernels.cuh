@@ -192,17 +192,17 @@ struct AdapterApply {
   uint64_t wait_limit_ns;
 };
 constexpr int64_t kAdapterMaxPairs = (int64_t(1) << 23) - 3;  // experts x adapters
-constexpr size_t kAdapterTilesAt = 64;  // byte offset of the tile count in the plan's header
+constexpr size_t kAdapterHeader = 256;  // of the plan, with
+constexpr size_t kAdapterTilesAt = 64;  // the byte offsets of the tile count in it
+constexpr size_t kAdapterTurnAt = 128;  // and of the counter that hands out the chunks
 size_t adapter_plan_bytes(const AdapterShape& s);
-// The plan's header (kAdapterHeader bytes) has to be zero where
-// adapter_plan_needs_clear says so (the launch of a small batch writes it);
-// status: where a bad adapter id is reported, the header's first word (the plan
-// itself) or a workspace's.
-bool adapter_plan_needs_clear(const AdapterShape& s);
-constexpr size_t kAdapterHeader = 256;
+// So many of the plan's first bytes have to be zero (none for a small batch,
+// whose launch writes its header); status: where a bad adapter id or an expired
+// wait is reported, the header's first word (the plan itself) or a workspace's.
+size_t adapter_plan_clear_bytes(const AdapterShape& s);
 cudaError_t launch_adapter_plan(const AdapterShape& s, const int32_t* offsets, const int32_t* perm,
-                                const int32_t* token_adapter, void* plan, int* status, bool chained,
-                                cudaStream_t stream);
+                                const int32_t* token_adapter, void* plan, int* status, uint64_t wait_limit_ns,
+                                bool chained, cudaStream_t stream);
 cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, bool chained, cudaStream_t stream);
 
 int device_sm_count();

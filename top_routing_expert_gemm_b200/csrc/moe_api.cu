@@ -334,7 +334,7 @@ cudaError_t run_adapted_ffn(const moe_config* c, const Carve& k, const moe_adapt
   const void* b1 = shared ? ad->b_gate_up_shared : ad->b_gate_up;
   const void* a2 = shared ? ad->a_down_shared : ad->a_down;
   const void* b2 = shared ? ad->b_down_shared : ad->b_down;
-  cudaError_t e = launch_adapter_plan(sh, offsets, perm, ad->token_adapter, plan, k.status, true, s);
+  cudaError_t e = launch_adapter_plan(sh, offsets, perm, ad->token_adapter, plan, k.status, wait_limit(c), true, s);
   if (e != cudaSuccess) return e;
   e = run_ffn(c, k, x, offsets, G, rows, f, w_gu, w_d, a1 ? pre : h, y, s, shared, a_quantized, true,
               a1 ? kFfnGemm1Plain : kFfnGemm1);
@@ -640,8 +640,10 @@ moe_status moe_adapter_plan(const moe_config* cfg, const moe_adapter_config* ad,
     return MOE_ERR_INVALID_ARG;
   DeviceGuard g;
   if ((st = enter(g, plan, stream)) != MOE_OK) return st;
-  if (s.rows == 0 || adapter_plan_needs_clear(s)) MOE_CUDA_TRY(cudaMemsetAsync(plan, 0, kAdapterHeader, stream));
-  MOE_CUDA_TRY(launch_adapter_plan(s, offsets, perm, token_adapter, plan, static_cast<int*>(plan), true, stream));
+  const size_t clear = adapter_plan_clear_bytes(s);
+  if (clear) MOE_CUDA_TRY(cudaMemsetAsync(plan, 0, clear, stream));
+  MOE_CUDA_TRY(launch_adapter_plan(s, offsets, perm, token_adapter, plan, static_cast<int*>(plan), wait_limit(cfg), true,
+                                   stream));
   return MOE_OK;
 }
 
@@ -698,10 +700,12 @@ moe_status moe_forward_routed(const moe_config* cfg, const moe_route_config* rou
   // everything that has to be zero is cleared ahead of the chain of launches (pdl.cuh)
   MOE_CUDA_TRY(cudaMemsetAsync(k.status, 0, 16, stream));
   if (k.counters) MOE_CUDA_TRY(cudaMemsetAsync(k.counters, 0, sizeof(int) * (size_t)k.counter_cap, stream));
-  if (rk.plan && adapter_plan_needs_clear(adapter_shape(cfg, adapters->n_adapters, adapters->rank, false)))
-    MOE_CUDA_TRY(cudaMemsetAsync(rk.plan, 0, kAdapterHeader, stream));
-  if (rk.plan_s && adapter_plan_needs_clear(adapter_shape(cfg, adapters->n_adapters, adapters->rank, true)))
-    MOE_CUDA_TRY(cudaMemsetAsync(rk.plan_s, 0, kAdapterHeader, stream));
+  for (int sh = 0; sh < 2; ++sh) {
+    void* plan = sh ? rk.plan_s : rk.plan;
+    const size_t clear =
+        plan ? adapter_plan_clear_bytes(adapter_shape(cfg, adapters->n_adapters, adapters->rank, sh != 0)) : 0;
+    if (clear) MOE_CUDA_TRY(cudaMemsetAsync(plan, 0, clear, stream));
+  }
   int32_t* ids = opt_topk_ids ? opt_topk_ids : k.ids;
   float* w = opt_topk_w ? opt_topk_w : k.w;
   int32_t* counts = opt_counts ? opt_counts : k.counts;
