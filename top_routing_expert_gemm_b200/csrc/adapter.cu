@@ -133,20 +133,18 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   grid_dependency_wait();  // the dispatch (programmatic launch)
   if (tid == 0) grid_launch_dependents();
-  int chunk = 0;
-  if (gridDim.x > 1) {
-    if (tid == 0) s_chunk = atomicAdd(p.turn, 1);
-    __syncthreads();
-    chunk = s_chunk;
-  }
-  const int64_t row0 = (int64_t)chunk * kChunkRows;
-  const int64_t row = row0 + tid;
-  const bool mine_to_load = tid < kChunkRows && row < p.rows;
+  const bool alone = gridDim.x == 1;
+  if (!alone && tid == 0) s_chunk = atomicAdd(p.turn, 1);
   bool bad = false;
-  const int slot = mine_to_load && p.perm ? p.perm[row] : 0;  // garbage behind the last row: not used there
+  // the row's slot (garbage behind the last row: not used there)
+  int slot = alone && p.perm && tid < kChunkRows && tid < p.rows ? p.perm[tid] : 0;
   if (p.offsets)
     for (int e = tid; e <= p.E; e += kPlanThreads) s_off[e] = p.offsets[e];
   __syncthreads();
+  const int chunk = alone ? 0 : s_chunk;
+  const int64_t row0 = (int64_t)chunk * kChunkRows;
+  const int64_t row = row0 + tid;
+  if (!alone && p.perm && tid < kChunkRows && row < p.rows) slot = p.perm[row];
   const int64_t live = p.offsets ? min((int64_t)s_off[p.E], p.rows) : p.rows;
   if (tid < kChunkRows) {
     int pair = kSkip;
@@ -878,11 +876,9 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
       for (int q = head.x; q < head.y; ++q) {
         if (ahead < Sh::kAhead && !f_over) fetch();
         if (ahead < Sh::kAhead && !f_over) fetch();  // until it is as far ahead as it may be
-        // this round's copies are the oldest of `ahead` groups
-        static_assert(Sh::kAhead <= 4, "one wait per depth");
-        if (ahead == 4) copies_wait<3>();
-        else if (ahead == 3) copies_wait<2>();
-        else if (ahead == 2) copies_wait<1>();
+        // the copies of round q are the oldest of `ahead` groups
+        static_assert(Sh::kAhead == 2, "one wait per depth");
+        if (ahead == 2) copies_wait<1>();
         else copies_wait<0>();
         const int c0 = q * CW;
         const bool work = c0 + warp * 32 < p.n_res;  // else the second group has none either
