@@ -213,7 +213,8 @@ def _find_current_stream():
     if raw is None:
         return lambda: torch.cuda.current_stream().cuda_stream
     torch.cuda.init()
-    return lambda: raw(torch.cuda.current_device())
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return lambda: raw(device())
 
 
 def _stream(stream) -> int | None:
