@@ -145,9 +145,9 @@ CASES = [
     dict(T=5, d=8, f=8, E=3, k=2, N=2, r=8, dtype="bf16"),
     dict(T=37, d=200, f=264, E=8, k=2, N=5, r=24, dtype="bf16"),
     dict(T=64, d=1000, f=520, E=8, k=2, N=64, r=16, dtype="bf16"),
-    dict(T=300, d=328, f=104, E=4, k=2, N=2, r=16, dtype="bf16", pattern="requests"),   # tiles of 64 rows
+    dict(T=300, d=328, f=104, E=4, k=2, N=2, r=16, dtype="bf16", pattern="requests"),
     dict(T=300, d=328, f=104, E=4, k=2, N=2, r=32, dtype="bf16"),
-    dict(T=257, d=136, f=72, E=2, k=2, N=3, r=64, dtype="bf16"),                        # tiles of 32 rows
+    dict(T=257, d=136, f=72, E=2, k=2, N=3, r=64, dtype="bf16"),
     dict(T=200, d=72, f=136, E=2, k=1, N=2, r=8, dtype="bf16", act="gelu"),
     dict(T=130, d=264, f=600, E=4, k=3, N=7, r=128, dtype="bf16", act="gelu"),
     dict(T=90, d=72, f=88, E=4, k=2, N=2, r=48, dtype="bf16", cap=20),

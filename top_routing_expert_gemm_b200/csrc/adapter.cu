@@ -14,8 +14,8 @@
 //           fixed order
 //   expand  base + s B U per tile and column block, then the activation
 // Measured (plan, shrink, expand): 2048 tokens, k = 2, 4096 -> 14336, 12 requests,
-// rank 16: 7.5, 12, 87 us; 8192 tokens, k = 4, 2880 -> 2880, 24 requests, rank 8: 10,
-// 41, 76; 64 tokens of 64 adapters, k = 2, 14336 -> 4096, rank 16: 6, 13, 12; one
+// rank 16: 8, 12, 86 us; 8192 tokens, k = 4, 2880 -> 2880, 24 requests, rank 8: 12,
+// 41, 75; 64 tokens of 64 adapters, k = 2, 14336 -> 4096, rank 16: 6, 13, 12; one
 // token, k = 2, 4096 -> 14336: 5, 4.5, 7.5.  Chained, a call takes 2 to 5 us less
 // than their sum.
 // Rows never meet; of the others in its batch a row's result depends by the
@@ -88,8 +88,8 @@ constexpr int kPlanThreads = 4 * kChunkRows;
 // before it: every block publishes its own number, and its first warp adds up
 // those before it, 32 at a time, down to one that has published its total.
 // Blocks take their chunks in turn, so whoever waits waits for running blocks.
-// (Places from one atomic counter took 6.3 us against 7.5 for 16 chunks and 7 against
-// 10 for 128, but then the order of the tiles, and with it the last bits of U,
+// (Places from one atomic counter took 6.3 us against 8 for 16 chunks and 7 against
+// 12 for 128, but then the order of the tiles, and with it the last bits of U,
 // changed from call to call.)
 constexpr unsigned long long kKnownOwn = 1, kKnownTotal = 2, kGivenUp = 3;  // low bits; the number above them
 __device__ __forceinline__ int64_t tiles_before(const PlanParams& p, int64_t chunk, int64_t own, int lane) {
