@@ -306,6 +306,50 @@ def test_route_backward_counts_of_zero_and_empty_terms():
     assert grad.eq(0).all()
 
 
+def _far_logits(dtype):
+    """Rows whose logits pass the end of fp32's exponential (88.72): every
+    quarter from 80 to 110 of either sign beside ordinary logits, beside its half,
+    and beside neighbours as far out."""
+    v = torch.cat([torch.arange(320, 441) / 4, -torch.arange(320, 441) / 4])
+    one = torch.ones_like(v)
+    rows = torch.cat([torch.stack([v, 0.25 * one, -1.5 * one, v / 2], 1), torch.stack([-1.5 * one, v, one, 3 * one], 1),
+                      torch.stack([v, v - 0.5, v - 1.0, v - 2.0], 1), torch.stack([v - 4.0, 0 * one, v, -v], 1)])
+    return rows.to(DT[dtype]).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_weights_of_logits_past_the_exponential_range(score, renorm, dtype):
+    """All four experts are picked, so the order is the logits' own and every
+    weight is checked.  Weights below 2^-126 may come out as 0 (the 1e-37)."""
+    l = _far_logits(dtype)
+    want_ids, want_w, _ = oracle.route_logits(_f64(l), None, 4, score, renormalise=bool(renorm), scale=2.5, dtype=dtype)
+    for rows in (l, _repeated(l)):
+        ids, w = _run(rows, None, _cfg(rows, 4, score, renorm=renorm, scale=2.5))
+        n = l.shape[0]
+        assert np.array_equal(ids[:n].cpu().numpy(), want_ids)
+        assert np.all(np.abs(_f64(w)[:n] - want_w) <= 80 * U * want_w + 1e-37)
+        if rows is not l:
+            assert torch.equal(ids[n:2 * n], ids[:n]) and torch.equal(w[n:2 * n], w[:n])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("z", [0.0, 0.25])
+def test_gradients_of_logits_past_the_exponential_range(score, renorm, dtype, z):
+    l = _far_logits(dtype)
+    T = l.shape[0]
+    cfg = _cfg(l, 4, score, renorm=renorm, scale=2.5)
+    ids, _ = _run(l, None, cfg)
+    g = torch.randn(T, 4, generator=torch.Generator().manual_seed(6)).cuda()
+    grad = torch.full_like(l, 77.0)
+    moe.moe_route_backward(cfg, l, ids, g, None, 0.0, z, grad)
+    torch.cuda.synchronize()
+    _grad_check(l, ids, g, cfg, score, None, 0.0, z, dtype, grad)
+
+
 # ------------------------------------------------------------------ combine
 def _dispatch(T, E, k, seed, cap=None):
     rng = np.random.default_rng(seed)

@@ -80,14 +80,16 @@ __device__ __forceinline__ float warp_max(float v) {
   asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
   return v;
 }
-// e^x to about 2^-21.5 of its value for any x (0 below 2^-126): the hardware's 2^t (2^-22) of the
-// rounded t = x log2 e, corrected by what the rounding left out
+// e^x: the hardware's 2^t (2^-22) of the rounded t = x log2 e, corrected by what the rounding left out,
+// about 2^-21.5 of the value.  From 88 on the correction is left out, since 2^t becomes infinite at 88.72
+// and inf * left is no number (such x only occur in 1 / (1 + e^x), below 2^-126 and flushed to 0);
+// below -87.34 the value is flushed to 0 and there is nothing to correct.
 __device__ __forceinline__ float exp_near(float x) {
   const float t = x * 1.4426950408889634f;
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
   const float left = fmaf(x, 1.4426950408889634f, -t);
-  return fabsf(x) < 100.0f ? fmaf(e, left * 0.6931471805599453f, e) : e;  // beyond, e is 0 or infinite
+  return fabsf(x) < 88.0f ? fmaf(e, left * 0.6931471805599453f, e) : e;
 }
 // 1 / x to 2^-23 (x of ordinary size, or infinite: 0)
 __device__ __forceinline__ float rcp_near(float x) {
