@@ -199,3 +199,21 @@ def test_adapter_struct_layouts():
     assert ctypes.sizeof(moe.MoeAdapterConfig) == 16
     assert ctypes.sizeof(moe.MoeAdapters) == 88 and moe.MoeAdapters.a_gate_up.offset == 24
     assert moe.moe_status_string(8) == "adapter id out of range"
+
+
+def test_pair_limit_of_the_routed_experts_holds_beside_shared_adapters(L):
+    """experts x adapters is limited for the routed experts' plan; the shared
+    expert's plan has one pair per adapter."""
+    cfg = _cfg(n_experts=1024, n_shared=1, d_ff_shared=512)
+    rc = _layer_route(cfg)
+    p, four = 256, dict(a_gate_up_shared=256, b_gate_up_shared=256, a_down_shared=256, b_down_shared=256)
+    routed = (dict(a_gate_up=p, b_gate_up=p), dict(a_down=p, b_down=p),
+              dict(a_gate_up=p, b_gate_up=p, a_down=p, b_down=p))
+    for n in (8192, 40000, 65536):
+        for part in routed:
+            for ad in (moe.make_adapters(n, 16, p, p, **part), moe.make_adapters(n, 16, p, p, **part, **four)):
+                assert moe.moe_forward_routed_workspace_bytes(cfg, ad) == 0
+                assert _forward(L, cfg, rc, ad, sgu=p, sd=p) == UNSUPPORTED
+        assert moe.moe_forward_routed_workspace_bytes(cfg, moe.make_adapters(n, 16, p, p, **four)) > 0
+    for part in routed:
+        assert moe.moe_forward_routed_workspace_bytes(cfg, moe.make_adapters(8191, 16, p, p, **part, **four)) > 0

@@ -308,10 +308,15 @@ RoutedCarve carve_routed(const moe_config* c, const moe_adapters* ad, void* base
 
 moe_status check_adapters(const moe_config* c, const moe_adapters* ad) {
   if (ad == nullptr) return MOE_OK;
+  // the routed and the shared experts have a plan each, with limits of their own
   const bool shared = ad->a_gate_up_shared || ad->b_gate_up_shared || ad->a_down_shared || ad->b_down_shared;
-  const moe_adapter_config ac{ad->n_adapters, ad->rank, shared ? 1 : 0, 0};
-  const moe_status st = check_adapter_config(c, &ac);
-  if (st != MOE_OK) return st;
+  const bool routed = ad->a_gate_up || ad->b_gate_up || ad->a_down || ad->b_down || !shared;
+  for (int sh = 0; sh < 2; ++sh) {
+    if (!(sh ? shared : routed)) continue;
+    const moe_adapter_config ac{ad->n_adapters, ad->rank, sh, 0};
+    const moe_status st = check_adapter_config(c, &ac);
+    if (st != MOE_OK) return st;
+  }
   const void* p[] = {ad->token_adapter, ad->scale,         ad->a_gate_up,        ad->b_gate_up,     ad->a_down,
                      ad->b_down,        ad->a_gate_up_shared, ad->b_gate_up_shared, ad->a_down_shared, ad->b_down_shared};
   for (const void* q : p)
