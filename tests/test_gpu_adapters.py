@@ -313,6 +313,31 @@ def test_shortest_wait_limit_is_right_or_reported_and_the_next_call_runs():
     c.check("gate_up")
 
 
+@pytest.mark.parametrize("which,r", [("gate_up", 8), ("gate_up", 128), ("down", 16), ("down", 64)])
+def test_expand_waits_that_expire_end_the_call(which, r):
+    """The plan is made with the usual limit, then the projection runs with 1 ns
+    several times over: a warp of the expand whose lanes do not see a wait expire
+    alike still leaves as one, so every call ends, right or with the status word
+    set, and the next plan and call are right."""
+    c = Case(T=1500, d=328, f=1032, E=4, k=2, N=3, r=r, dtype="bf16").tensors(which)
+    usual = c.cfg.wait_limit_ns
+    for _ in range(6):
+        c.out.fill_(5.5)
+        plan = c.plan()
+        c.cfg.wait_limit_ns = 1
+        c.call(which, plan)
+        c.cfg.wait_limit_ns = usual
+        st = moe.moe_device_status(plan)
+        assert st in (0, moe.MOE_ERR_TIMEOUT)
+        if st == 0:
+            c.check(which)
+    c.out.fill_(5.5)
+    plan = c.plan()
+    c.call(which, plan)
+    assert moe.moe_device_status(plan) == 0
+    c.check(which)
+
+
 def test_plan_of_a_batch_with_long_runs_and_single_rows():
     """Chunks of the plan that end inside runs, tiles that end inside chunks: 700
     rows of one adapter, then every row another, then none."""

@@ -851,10 +851,16 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
       f_slot = (f_slot + 1) % Sh::kAhead;
       return true;
     };
+    // The lanes wait each for itself (so each sees what the barrier guards) and
+    // go on or leave together: one whose limit expired must not part from those
+    // that the shuffles, the MMAs and the block's barrier below wait for.
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(kFull, tc::mbar_wait_bounded(tc::smem_u32(bar), parity, abort_flag, p.wait_limit_ns, p.status));
+    };
     int slot = 0;
     bool ok = true;
     while (ok) {
-      ok = tc::mbar_wait_bounded(tc::smem_u32(&hd->ifull[info]), info_phase, abort_flag, p.wait_limit_ns, p.status);
+      ok = wait(&hd->ifull[info], info_phase);
       if (!ok) break;
       const TileInfo<RK>& ti = infos[info];
       const int4 head = *reinterpret_cast<const int4*>(&ti);
@@ -901,7 +907,7 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
         slot = (slot + 1) % Sh::kAhead;
         --ahead;
         if (has) {
-          ok = tc::mbar_wait_bounded(tc::smem_u32(&hd->full[stage]), phase, abort_flag, p.wait_limit_ns, p.status);
+          ok = wait(&hd->full[stage], phase);
           if (!ok) break;
           if (work) {
             const uint8_t* st =
