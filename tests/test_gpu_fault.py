@@ -38,6 +38,24 @@ def test_expired_wait_limit_reports_timeout_and_context_survives(cfg):
     H.check_forward(inp, good)
 
 
+@pytest.mark.parametrize("cfg", [
+    synth.LayerConfig("again", 1024, 1024, 8, 2, 1024, "bf16", synth.SOFTMAX_TOPK, seed=25),
+    synth.LayerConfig("again_router_tc", 512, 2048, 64, 2, 1024, "bf16", synth.SOFTMAX_TOPK, seed=26),
+], ids=lambda c: c.name)
+def test_calls_with_an_expired_limit_end_over_and_over(cfg):
+    """Whether a wait is over at a lane's first looks changes from call to call:
+    every call ends, right or with the status word set."""
+    inp = H.make_inputs(cfg)
+    for _ in range(10):
+        out = H.run_forward(inp, wait_limit_ns=1)
+        assert out["status"] in (0, moe.MOE_ERR_TIMEOUT)
+        if out["status"] == 0:
+            H.check_forward(inp, out)
+    good = H.run_forward(inp)
+    assert good["status"] == 0
+    H.check_forward(inp, good)
+
+
 def test_injected_launch_failure_launches_nothing_and_the_next_call_runs(monkeypatch):
     """MOE_FAULT=launch (a host-side hook; nothing is injected on the device):
     every launching entry point reports MOE_ERR_CUDA, its outputs keep their

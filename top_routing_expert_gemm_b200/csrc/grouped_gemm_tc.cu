@@ -343,7 +343,11 @@ __global__ void __launch_bounds__(kThreads<FP8, MODE>, 1)
     for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
       int g, mt, ntile;
       decode_tile(t, p.nt, s_cum, G, g, mt, ntile);
-      if (!mbar_wait_bounded(smem_u32(&tfull[acc]), acc_phase, abort_flag, p.wait_limit_ns, p.status)) break;
+      // a warp's lanes go on or leave together: the tensor memory loads and the
+      // shuffles below take whole warps, and no limit ends a wait for the others
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&tfull[acc]), acc_phase, abort_flag, p.wait_limit_ns,
+                                                     p.status)))
+        break;
       tc_fence_after();
       const int rows_g = s_off[g + 1] - s_off[g];
       const int lr = mt * BM + r;
@@ -451,7 +455,8 @@ __global__ void __launch_bounds__(kThreads<FP8, MODE>, 1)
                                    __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
         }
         mbar_arrive(smem_u32(lrdy));
-        const bool lok = mbar_wait_bounded(smem_u32(lrdy), l_phase, abort_flag, p.wait_limit_ns, p.status);
+        const bool lok = __all_sync(
+            0xffffffffu, mbar_wait_bounded(smem_u32(lrdy), l_phase, abort_flag, p.wait_limit_ns, p.status));
         l_phase ^= 1u;
         if (!lok) break;
         constexpr int R = 4;                       // rows in flight per warp
