@@ -442,7 +442,8 @@ size_t moe_adapter_plan_bytes(const moe_config* cfg, const moe_adapter_config* a
    calls below read and use (it holds their partial sums), valid for as long as
    the batch's rows are; calls that share a plan must not overlap.  This call
    clears the status word; an expired wait of this call or of the calls below is
-   recorded there (MOE_ERR_TIMEOUT).  Runs on the device of plan. */
+   recorded there (MOE_ERR_TIMEOUT; after one of this call's own the calls below
+   write nothing on this plan).  Runs on the device of plan. */
 moe_status moe_adapter_plan(const moe_config* cfg, const moe_adapter_config* ad, const int32_t* offsets,
                             const int32_t* perm, const int32_t* token_adapter, void* plan, size_t plan_bytes,
                             moe_stream_t stream);

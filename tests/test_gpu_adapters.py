@@ -338,6 +338,52 @@ def test_expand_waits_that_expire_end_the_call(which, r):
     c.check(which)
 
 
+@pytest.mark.parametrize("dtype,T", [("bf16", 40), ("bf16", 700), ("f32", 40), ("f32", 700)])
+@pytest.mark.parametrize("which", ["gate_up", "down"])
+def test_a_plan_that_gave_up_is_not_used(which, dtype, T):
+    """A chunk of the plan whose wait expired leaves its tiles unwritten and marks
+    the plan in the word behind the tile count (byte 68); here a whole plan is
+    marked by hand.  The projections then write nothing, and a new plan serves."""
+    c = Case(T=T, d=264, f=136, E=4, k=2, N=3, r=16, dtype=dtype).tensors(which)
+    plan = c.plan()
+    head = plan[64:72].view(torch.int32)
+    assert head[0] > 0 and head[1] == 0
+    head[1] = 1
+    c.call(which, plan)
+    torch.cuda.synchronize()
+    assert c.out.eq(5.5).all()
+    moe.moe_adapter_plan(c.cfg, c.ad, c.offsets, c.perm, c.ta, plan)
+    c.call(which, plan)
+    assert moe.moe_device_status(plan) == 0
+    c.check(which)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_plan_waits_that_expire_leave_a_void_plan_or_a_right_one(dtype):
+    """47 chunks with a limit of 1 ns: a plan whose chunks gave up says so and is
+    not used, any other is right, and the next call (the usual limit) is right."""
+    c = Case(T=6000, d=64, f=96, E=4, k=2, N=9, r=8, dtype=dtype).tensors("down")
+    plan = c.plan()
+    c.call("down", plan)
+    want = c.out.clone()
+    usual = c.cfg.wait_limit_ns
+    for _ in range(40):
+        c.out.fill_(5.5)
+        c.cfg.wait_limit_ns = 1
+        moe.moe_adapter_plan(c.cfg, c.ad, c.offsets, c.perm, c.ta, plan)
+        c.cfg.wait_limit_ns = usual
+        st = moe.moe_device_status(plan)
+        assert st in (0, moe.MOE_ERR_TIMEOUT)
+        assert (plan[64:72].view(torch.int32)[1] != 0) == (st != 0)
+        c.call("down", plan)
+        assert c.out.eq(5.5).all() if st else torch.equal(c.out, want)
+    c.out.fill_(5.5)
+    plan = c.plan()
+    c.call("down", plan)
+    assert moe.moe_device_status(plan) == 0
+    c.check("down")
+
+
 def test_plan_of_a_batch_with_long_runs_and_single_rows():
     """Chunks of the plan that end inside runs, tiles that end inside chunks: 700
     rows of one adapter, then every row another, then none."""

@@ -70,7 +70,7 @@ struct PlanParams {
   int64_t rows;
   int E, k, N;
   Tile* tiles;
-  int* n_tiles;
+  int2* n_tiles;             // the number of tiles; not 0: a chunk gave up
   int* turn;                 // several blocks: which chunk is next,
   unsigned long long* state; // and what is known of each (kKnown...)
   int* status;
@@ -118,7 +118,12 @@ __device__ __forceinline__ int64_t tiles_before(const PlanParams& p, int64_t chu
     if (lost) break;
   }
   if (lane == 0) {
-    if (lost) set_status(p.status, kDevTimeout);
+    if (lost) {
+      // This chunk's tiles will be missing, and a later chunk that has already
+      // read its number counts them: the whole plan is void.
+      p.n_tiles->y = 1;
+      set_status(p.status, kDevTimeout);
+    }
     state[chunk] = lost ? kGivenUp : (unsigned long long)(before + own) << 2 | kKnownTotal;
   }
   return lost ? -1 : before;
@@ -226,7 +231,8 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
     const int64_t before = gridDim.x > 1 ? tiles_before(p, chunk, n, lane) : 0;
     __syncwarp();
     if (lane == 0) {
-      if (chunk == (int)gridDim.x - 1) *p.n_tiles = before < 0 ? 0 : (int)before + n;  // 0: nothing is done
+      if (chunk == (int)gridDim.x - 1) p.n_tiles->x = before < 0 ? 0 : (int)before + n;
+      if (gridDim.x == 1) p.n_tiles->y = 0;  // otherwise cleared ahead of the launch
       s_base = (int)before;
       n = 0;
       for (int w = 0; w < kChunkRows / 32; ++w) {
@@ -249,12 +255,19 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
   }
 }
 
+// The tiles of a plan as the kernels that use it see them: none if a chunk gave
+// up, since some of those counted were then never written.
+__device__ __forceinline__ int planned_tiles(const int2* n_tiles) {
+  const int2 n = *n_tiles;
+  return n.y ? 0 : n.x;
+}
+
 // ---------------------------------------------------------------- shrink
 struct ShrinkParams {
   const void* x;  // [rows, K]
   const void* a;  // [N, E, r, K]
   const Tile* tiles;
-  const int* n_tiles;
+  const int2* n_tiles;
   float* u;       // [rows][r]: a tile's first partial sum, by tile.start
   float* more;    // [blocks][16][r]: the partial sums that continue a tile
   int K, r, E;
@@ -361,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) adapter_shrink_kern
   if (threadIdx.x == 0) grid_launch_dependents();
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
   const int units = (p.K + kUnitInputs - 1) / kUnitInputs;
-  const Run run = run_of((int64_t)*p.n_tiles * units, blockIdx.x, gridDim.x);
+  const Run run = run_of((int64_t)planned_tiles(p.n_tiles) * units, blockIdx.x, gridDim.x);
 
   // a piece of the run is a tile's units, or what the run has of them.  The one
   // that starts at `at` is looked at while the one before it is computed:
@@ -490,7 +503,7 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_f32_kernel(const Shri
   const float* x = static_cast<const float*>(p.x);
   const int ranks = p.r / 8;
   const int k_units = (p.K + kUnitInputs - 1) / kUnitInputs;
-  const Run run = run_of((int64_t)*p.n_tiles * k_units, blockIdx.x, gridDim.x);
+  const Run run = run_of((int64_t)planned_tiles(p.n_tiles) * k_units, blockIdx.x, gridDim.x);
   for (int64_t at = run.lo; at < run.hi;) {
     const int t = (int)quotient(at, k_units);
     const int* rows = p.tiles[t].rows;
@@ -554,7 +567,7 @@ struct ExpandParams {
   const void* base;  // [rows, n_out]
   void* out;         // [rows, f] (SwiGLU: n_out = 2 f) or [rows, n_out]
   const Tile* tiles;
-  const int* n_tiles;
+  const int2* n_tiles;
   int64_t rows;
   int r, E;
   int units, shrink_blocks;  // the shrink's units per tile and its blocks
@@ -713,7 +726,7 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
   if (warp == kWarps) {
     // ------------------------------------------------ producer
     const int rounds = (p.n_res + CW - 1) / CW;  // per tile
-    const int n_tiles = *p.n_tiles;
+    const int n_tiles = planned_tiles(p.n_tiles);
     const Run run = run_of((int64_t)n_tiles * rounds, blockIdx.x, gridDim.x);
     for (int64_t at = run.lo;;) {
       const bool over = at >= run.hi;
@@ -974,7 +987,7 @@ __global__ void __launch_bounds__(kThreads) adapter_expand_f32_kernel(const Expa
   __shared__ int srow[kTileRows];
   grid_dependency_wait();
   if (threadIdx.x == 0) grid_launch_dependents();
-  const int n_tiles = *p.n_tiles;
+  const int n_tiles = planned_tiles(p.n_tiles);
   const float* base = static_cast<const float*>(p.base);
   float* out = static_cast<float*>(p.out);
   for (int t = blockIdx.y; t < n_tiles; t += gridDim.y) {
@@ -1137,7 +1150,7 @@ cudaError_t launch_adapter_plan(const AdapterShape& s, const int32_t* offsets, c
   if (s.rows == 0) return cudaSuccess;
   const unsigned blocks = (unsigned)chunks_of(s);
   PlanParams p{offsets, perm, token_adapter, s.rows, s.E, s.k, s.N, reinterpret_cast<Tile*>(base + l.tiles),
-               reinterpret_cast<int*>(base + kAdapterTilesAt), reinterpret_cast<int*>(base + kAdapterTurnAt),
+               reinterpret_cast<int2*>(base + kAdapterTilesAt), reinterpret_cast<int*>(base + kAdapterTurnAt),
                reinterpret_cast<unsigned long long*>(base + l.state), status, wait_limit_ns, blocks == 1 && status == plan};
   return launch_maybe_chained(adapter_plan_kernel, dim3(blocks), dim3(kPlanThreads), sizeof(int) * (size_t)(s.E + 1),
                               stream, chained, p);
@@ -1155,7 +1168,7 @@ cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, b
   const int n_res = a.gate_up ? s.f : s.d;
   const int n_out = a.gate_up && s.act == kEpiSwiGLU ? 2 * s.f : n_res;
   const Tile* tiles = reinterpret_cast<const Tile*>(base + l.tiles);
-  const int* n_tiles = reinterpret_cast<const int*>(base + kAdapterTilesAt);
+  const int2* n_tiles = reinterpret_cast<const int2*>(base + kAdapterTilesAt);
   float* u = reinterpret_cast<float*>(base + l.u);
   float* more = reinterpret_cast<float*>(base + l.more);
   const int blocks = shrink_blocks(s), units = (K + kUnitInputs - 1) / kUnitInputs;

@@ -193,7 +193,8 @@ struct AdapterApply {
 };
 constexpr int64_t kAdapterMaxPairs = (int64_t(1) << 23) - 3;  // experts x adapters
 constexpr size_t kAdapterHeader = 256;  // of the plan, with
-constexpr size_t kAdapterTilesAt = 64;  // the byte offsets of the tile count in it
+constexpr size_t kAdapterTilesAt = 64;  // the byte offsets of the tile count in it (and, in the word
+                                        // behind, whether a chunk gave up, so that tiles may be missing)
 constexpr size_t kAdapterTurnAt = 128;  // and of the counter that hands out the chunks
 size_t adapter_plan_bytes(const AdapterShape& s);
 // So many of the plan's first bytes have to be zero (none for a small batch,
