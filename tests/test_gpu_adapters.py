@@ -397,6 +397,48 @@ def test_plan_of_a_batch_with_long_runs_and_single_rows():
     c.check("down")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("which,act", [("down", "swiglu"), ("gate_up", "swiglu"), ("gate_up", "gelu")])
+def test_infinite_inputs_and_products_give_what_the_formula_gives(which, act, dtype):
+    """Row by row: an infinite input, products of finite inputs that pass fp32's
+    range, sums between bf16's largest value and fp32's, an infinite base, and a
+    NaN input; the other rows are as without them."""
+    c = Case(T=40, d=64, f=72, E=2, k=1, N=1, r=16, dtype=dtype, act=act, pattern="one").tensors(which)
+    c.a.abs_()
+    c.b.abs_().clamp_(min=0.01)
+    c.a[..., :2] = 1.9921875
+    c.x.abs_()
+    c.scale.fill_(1.0)
+    x, base = c.x, c.base
+    clean = c.plan()
+    c.call(which, clean)
+    usual = c.out.clone()
+    top = 3.3895313892515355e38
+    x[3, 5] = float("inf")
+    x[4, :2] = top                              # U = 1.35e39, infinite in fp32
+    base[6] = float("inf")
+    x[7, 1] = float("nan")
+    x[8] = 0.0
+    x[8, 0], x[8, 1] = 2.0 ** 127, 5e35         # U = 3.40e38: more than bf16's largest, less than fp32's
+    c.call(which, clean)
+    assert c.out[[3, 4, 6]].eq(float("inf")).all()
+    assert c.out[7].isnan().all()
+    rest = torch.tensor([i for i in range(40) if i not in (3, 4, 6, 7, 8)], device="cuda")
+    assert torch.equal(c.out[rest], usual[rest])
+    # the sum of row 8: small weights keep its result in range
+    c.b.mul_(2.0 ** -100)
+    c.call(which, clean)
+    e = int(c.expert[8])
+    delta = _f64(c.b[0, e]) @ (_f64(c.a[0, e]) @ _f64(x[8]))
+    v = _f64(base[8]) + delta
+    assert np.all(delta > 1e6) and np.abs(_f64(c.a[0, e]) @ _f64(x[8])).max() > top * (1 + 2.0 ** -9)
+    f = c.f
+    want = v if which == "down" else v[:f] * v[f:] if act == "swiglu" else v  # silu and gelu are the identity here
+    # U: two products, one addition; as two bf16 values; r products; the rounding
+    tol = 2 * (4 * U + 2.0 ** -17 + 16 * 4 * U + 20 * U) + HALF_STEP[dtype]
+    assert np.all(np.abs(_f64(c.out[8]) - want) <= tol * np.abs(want))
+
+
 # ------------------------------------------------------------------ the layer
 def _layer(T, d, f, E, k, dtype, n_shared=0, act="swiglu", seed=0, e4m3=False, cap=0.0):
     gen = torch.Generator().manual_seed(seed)

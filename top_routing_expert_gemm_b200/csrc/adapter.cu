@@ -647,6 +647,13 @@ __device__ __forceinline__ uint32_t finish_bf16(float2 v, float2 up) {
 // leaves in 16-byte vectors.  base is the accumulators' first value.  U enters
 // as a sum of two bf16 values (16 bits of mantissa), so its rounding does not
 // show beside the result's own.
+//
+// The first of the two values is kept finite, so that the second, what is left
+// of U, is infinite or NaN where U is, and not inf - inf.
+__device__ __forceinline__ float in_bf16(float v) {
+  constexpr float kMost = 3.38953138925153547590e38f;
+  return fminf(fmaxf(v, -kMost), kMost);
+}
 constexpr int kMaxStages = 8;
 constexpr int kInfos = 4;  // tiles the producer may be ahead
 struct ExpandHeader {
@@ -770,8 +777,8 @@ __global__ void __launch_bounds__(kExpandThreads, expand_blocks<RK, EPI>())
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float4 v = u[c][h];
-            hi[h] = pack_bf16x2(v.x, v.y);
-            hi[2 + h] = pack_bf16x2(v.z, v.w);
+            hi[h] = pack_bf16x2(in_bf16(v.x), in_bf16(v.y));
+            hi[2 + h] = pack_bf16x2(in_bf16(v.z), in_bf16(v.w));
             const __nv_bfloat162 p0 = *reinterpret_cast<__nv_bfloat162*>(&hi[h]);
             const __nv_bfloat162 p1 = *reinterpret_cast<__nv_bfloat162*>(&hi[2 + h]);
             lo[h] = pack_bf16x2(v.x - __low2float(p0), v.y - __high2float(p0));
