@@ -358,6 +358,23 @@ def test_a_plan_that_gave_up_is_not_used(which, dtype, T):
     c.check(which)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(T=700, d=520, f=328, E=4, k=2, N=3, r=48, dtype="bf16", pattern="requests"),
+    dict(T=900, d=1032, f=264, E=2, k=2, N=2, r=64, dtype="bf16", pattern="requests"),
+    dict(T=1200, d=264, f=840, E=1, k=1, N=3, r=88, dtype="bf16", shared=True, pattern="requests"),
+    dict(T=600, d=648, f=520, E=4, k=2, N=5, r=128, dtype="bf16", act="gelu"),
+    dict(T=1100, d=136, f=200, E=2, k=1, N=2, r=128, dtype="f32", pattern="requests"),
+], ids=lambda kw: "-".join(str(v) for v in kw.values()))
+@pytest.mark.parametrize("which", ["gate_up", "down"])
+def test_high_ranks_over_many_tiles(which, kw):
+    """Ranks above 32 over batches of several chunks, with full tiles of long runs."""
+    c = Case(**kw).tensors(which)
+    plan = c.plan()
+    c.call(which, plan)
+    assert moe.moe_device_status(plan) == 0
+    c.check(which)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_plan_waits_that_expire_leave_a_void_plan_or_a_right_one(dtype):
     """47 chunks with a limit of 1 ns: a plan whose chunks gave up says so and is
@@ -507,6 +524,44 @@ def test_layer_without_adapters_is_the_chain_of_its_stages(T, dtype, n_shared, c
     assert torch.equal(counts, c2) and torch.equal(y, want)
     if not n_shared:
         assert y[T // 2].eq(0).all()
+
+
+@pytest.mark.parametrize("T,E,k", [(2048, 256, 8), (1500, 60, 2), (400, 256, 4), (9000, 16, 2)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_layer_of_many_experts_with_empty_slots(T, E, k, e4m3):
+    """Dispatches of several chunks (and of one, for the 400 tokens) with slots
+    that no expert is left for: masked tokens, and tokens with fewer experts than
+    slots.  Empty slots are no error, and the layer is what its stages make of the
+    slots there are."""
+    cfg, route, t = _layer(T, 128, 64, E, k, "bf16", e4m3=e4m3)
+    g = torch.Generator().manual_seed(T)
+    t["logits"][(torch.rand(T, generator=g) < 0.2).cuda()] = float("-inf")
+    t["logits"][:, :E - 1] = t["logits"][:, :E - 1].masked_fill(
+        (torch.rand(T, 1, generator=g) < 0.1).cuda(), torch.finfo(torch.float32).min)  # one expert left
+    if e4m3:
+        t["w_gu_q"], t["w_d_q"], t["s_gu_q"], t["s_d_q"] = _blob(t["w_gu"]), _blob(t["w_d"]), None, None
+    names = ("w_gu_q", "w_d_q", "s_gu_q", "s_d_q") if e4m3 else ("w_gu", "w_d", "s_gu", "s_d")
+    y, ids, w, counts, ws = _forward(cfg, route, t, None, names)
+    assert moe.moe_device_status(ws) == 0
+    empty = ids.eq(-1)
+    assert empty.any() and (empty.sum(1) == k - 1).any() and w[empty].eq(0).all()
+    used = ids[~empty].long()
+    assert torch.equal(counts.long(), torch.bincount(used, minlength=E))
+    # the stages, every empty slot sent to expert 0 with weight 0
+    ids2 = torch.where(empty, torch.zeros_like(ids), ids)
+    ws2 = torch.zeros(moe.moe_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    c2, off = torch.empty_like(counts), torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    perm, row_of = (torch.empty(T * k, dtype=torch.int32, device="cuda") for _ in range(2))
+    xp, yp = (torch.zeros(T * k, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    moe.moe_permute(cfg, ids2, t["x"], c2, off, perm, row_of, xp, ws2)
+    moe.moe_grouped_ffn(cfg, xp, off, t[names[0]], t[names[1]], yp, ws2)
+    want = torch.empty_like(y)
+    moe.moe_combine(cfg, yp, row_of, w, None, want)
+    assert moe.moe_device_status(ws2) == 0
+    assert y[empty.all(1)].eq(0).all()
+    # the same rows in other tiles: sums over k terms of products accumulated in another order, h and y_perm
+    # rounded to bf16 (the layer's tolerance)
+    assert float((y.float() - want.float()).abs().max()) <= 2e-2 * float(want.float().abs().max())
 
 
 def _adapters(cfg, N, r, dtype, gen, shared, act="swiglu", std=0.5):

@@ -306,6 +306,28 @@ def test_route_backward_counts_of_zero_and_empty_terms():
     assert grad.eq(0).all()
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("balance,z", [(0.0, 0.0), (0.5, 0.25)])
+def test_gradients_of_repeated_and_stray_ids_match_the_oracle(score, renorm, balance, z):
+    """Every slot of a repeated id counts with its own gradient, a stray id is an
+    empty slot, a masked expert's slot adds nothing, with the penalties or without."""
+    l = torch.randn(7, 10, generator=torch.Generator().manual_seed(4))
+    l[2, 5] = float("-inf")
+    l[6] = float("-inf")
+    l = l.cuda()
+    ids = torch.tensor([[1, 1, 3], [0, 9, 10], [5, 2, 1], [-1, -1, -1], [7, -3, 7], [2 ** 30, 4, 4], [3, 3, 8]],
+                       dtype=torch.int32, device="cuda")
+    g = torch.randn(7, 3, generator=torch.Generator().manual_seed(5)).cuda()
+    counts = torch.arange(10, dtype=torch.int32, device="cuda")
+    cfg = _cfg(l, 3, score, renorm=renorm, scale=2.5)
+    grad = torch.full_like(l, 77.0)
+    moe.moe_route_backward(cfg, l, ids, g, counts if balance else None, balance, z, grad)
+    torch.cuda.synchronize()
+    _grad_check(l, ids, g, cfg, score, counts, balance, z, "f32", grad)
+    assert grad[6].eq(0).all() and grad[2, 5] == 0
+
+
 def _far_logits(dtype):
     """Rows whose logits pass the end of fp32's exponential (88.72): every
     quarter from 80 to 110 of either sign beside ordinary logits, beside its half,
