@@ -219,6 +219,35 @@ def test_biases_past_the_range_of_fp32(score, b, G, want):
         assert torch.allclose(w.cpu(), (share / share.sum()).expand(T, -1))
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k,G,Gk,gtop", [(64, 8, 8, 3, 2), (64, 6, 8, 2, 1), (30, 5, 5, 2, 2), (256, 12, 8, 4, 2),
+                                           (40, 4, 1, 1, 1)])
+@pytest.mark.parametrize("span", [24, 60, 120])
+def test_saturated_scores_rank_by_their_logits(score, E, k, G, Gk, gtop, span):
+    """Without a bias, or with zeros, scores that are equal in binary64 (sigmoids of
+    logits above 37, differences of a denominator's last bit) still rank by the
+    logits; whole numbers, so that logits tie too, and then the lower index wins.
+    A group's sum of two is compared as a sum: equal ones keep the lower group; where
+    its one best counts, that one's logit does, so the picks are those of a tenth
+    of the logits, which does not saturate."""
+    l = torch.randint(-span // 4, span + 1, (48, E), generator=torch.Generator().manual_seed(E + span)).float().cuda()
+    l[5] = 50.0
+    l[6, ::3] = float("-inf")
+    want, want_w, _ = oracle.route_logits(_f64(l), None, k, score, G, Gk, gtop)
+    if gtop == 1:
+        want, _, _ = oracle.route_logits(0.1 * _f64(l), None, k, score, G, Gk, gtop)
+        ls = np.vectorize(lambda v: -np.logaddexp(0.0, -v))(_f64(l)) if score == "sigmoid" else _f64(l)
+        w = np.exp(np.take_along_axis(ls, want, 1) - np.take_along_axis(ls, want, 1).max(1, keepdims=True))
+        want_w = w / w.sum(1, keepdims=True)
+    many = _repeated(l)
+    for bias in (None, torch.zeros(E, device="cuda")):
+        ids, w = _run(l, bias, _cfg(l, k, score, G, Gk, gtop))
+        assert np.array_equal(ids.cpu().numpy(), want)
+        assert np.all(np.abs(_f64(w) - want_w) <= 80 * U * want_w + 1e-37)
+        ids2, _ = _run(many, bias, _cfg(many, k, score, G, Gk, gtop))
+        assert torch.equal(ids2[:48], ids) and torch.equal(ids2[48 * 170:48 * 171], ids)
+
+
 def test_rows_past_32_bit_offsets():
     """Row strides that take the last rows past 2^32 bytes and 2^31 elements."""
     T, E, stride = 2100, 16, 1 << 20

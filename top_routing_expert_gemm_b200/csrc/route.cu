@@ -155,12 +155,12 @@ template <> __device__ __forceinline__ float neg_inf<float>() { return -INFINITY
 template <> __device__ __forceinline__ double neg_inf<double>() { return -(double)INFINITY; }
 
 // The picks of one row for any group shape, from the choices c (-inf: not to
-// be picked) of the warp's columns.  Lane s < k returns slot s (-1: none
-// left).  near: two values whose order decides something were within eps
+// be picked) of the warp's columns; the groups kept, the experts rank by them, or
+// by their logits (row, not null).  Lane s < k returns slot s (-1: none left).  near: two values whose order decides something were within eps
 // (group scores: 2 eps).  Used in fp32 where a group is no aligned run of
 // lanes, and in binary64 for the rows whose fp32 decision was too close.
-template <typename F, int NC>
-__device__ __noinline__ int pick_any(F (&c)[NC], const RouteArgs& p, int lane, F eps, bool* near) {
+template <typename T, typename F, int NC>
+__device__ __noinline__ int pick_any(F (&c)[NC], const T* row, const RouteArgs& p, int lane, F eps, bool* near) {
   bool close = false;
   const int c0 = lane * NC;
   if (p.G > 1) {
@@ -199,6 +199,11 @@ __device__ __noinline__ int pick_any(F (&c)[NC], const RouteArgs& p, int lane, F
 #pragma unroll
     for (int j = 0; j < NC; ++j)
       if (c0 + j < p.E && !(kept >> ((c0 + j) / gs) & 1u)) c[j] = neg_inf<F>();
+  }
+  if (row) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (c[j] > neg_inf<F>()) c[j] = (F)usable<T>(Elem<T>::to_f(row[c0 + j]));
   }
   int id = -1;
   F prev = (F)INFINITY;
@@ -295,18 +300,23 @@ __device__ __forceinline__ int pick_candidates(const uint32_t (&key)[NC], const 
 }
 
 // The row again in binary64: scores from the fp32 or bf16 logits as stored.
-// runs: groups are aligned runs of lanes_g lanes.
+// runs: groups are aligned runs of lanes_g lanes.  Without a bias, or with zeros
+// (and groups by sums of two, or nothing would be close), the groups kept, the
+// experts rank by their logits, which differ where saturated scores do not.
 template <typename T, int NC>
 __device__ __noinline__ int pick_exact(const RouteArgs& p, const T* row, int lane, bool runs, int lanes_g,
                                        Picks<double>* cand, Picks<double>* order) {
   const int c0 = lane * NC;
   double c[NC];
+  bool zero = true;
   double m = -(double)INFINITY;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     c[j] = c0 + j < p.E ? (double)usable<T>(Elem<T>::to_f(row[c0 + j])) : -(double)INFINITY;
     m = fmax(m, c[j]);
+    zero &= !p.bias || c0 + j >= p.E || p.bias[c0 + j] == 0.f;
   }
+  zero = __all_sync(kFull, zero);
   double z = 0.0;
   if (!p.sigmoid) {
 #pragma unroll
@@ -345,26 +355,31 @@ __device__ __noinline__ int pick_exact(const RouteArgs& p, const T* row, int lan
       kept = c0 < p.E && rank < p.Gk;
     }
     uint32_t key[NC];
+    double by[NC];
 #pragma unroll
-    for (int j = 0; j < NC; ++j) key[j] = kept ? key_of(fmaxf((float)c[j], c[j] > -(double)INFINITY ? lowest<float>() : -INFINITY)) : 0u;
-    const int n = pick_candidates<double, NC>(key, c, p.k, c0, lane, cand, order);
+    for (int j = 0; j < NC; ++j) {
+      const bool in = kept && c[j] > -(double)INFINITY;
+      double v = c[j];
+      if (in && zero) v = (double)usable<T>(Elem<T>::to_f(row[c0 + j]));
+      key[j] = in ? key_of(fmaxf((float)v, lowest<float>())) : 0u;
+      by[j] = v;
+    }
+    const int n = pick_candidates<double, NC>(key, by, p.k, c0, lane, cand, order);
     if (n <= 32) {
       const int id = lane < min(n, p.k) ? order->col[lane] : -1;
       __syncwarp();
       return id;
     }
   }
-  double v[NC];
-#pragma unroll
-  for (int j = 0; j < NC; ++j) v[j] = c[j];
   bool unused;
-  return pick_any<double, NC>(v, p, lane, 0.0, &unused);
+  return pick_any<T, double, NC>(c, zero ? row : nullptr, p, lane, 0.0, &unused);
 }
 
 // The picks of a row whose kept groups are certain but whose order is not: only
 // the columns within reach of the k-th best, vk, can be picked, so only those
 // (one per lane, seldom more than k + 2) are computed in binary64.  thr: vk less
-// the bound; m, inv: the softmax's maximum and 1 / denominator.  Returns the
+// the bound; m, inv: the softmax's maximum and 1 / denominator.  Without a bias
+// they rank by their logits (pick_exact).  Returns the
 // number of candidates; over 32, nothing is decided.  Not unrolled: it runs for
 // one row in a thousand, and its instructions come from far away.
 template <typename T>
@@ -373,6 +388,7 @@ __device__ __noinline__ int pick_near(const RouteArgs& p, const T* row, int lane
   const int gs = p.E / p.G;
   int n = 0;
   double z = 0.0;
+  bool zero = true;
 #pragma unroll 1
   for (int c0 = 0; c0 < p.E; c0 += 256) {  // 256 columns' loads in flight: the row is in L2 at best
     float l[8], b[8];
@@ -385,6 +401,7 @@ __device__ __noinline__ int pick_near(const RouteArgs& p, const T* row, int lane
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = c0 + 32 * j + lane;
+      zero &= b[j] == 0.f;
       const float v = (p.sigmoid ? sigmoid_fast(l[j]) : __expf(l[j] - m) * inv) + b[j];
       const bool in = l[j] > -INFINITY && v > -INFINITY && v >= thr && (p.G == 1 || kept >> (c / gs) & 1u);
       const unsigned who = __ballot_sync(kFull, in);
@@ -402,12 +419,13 @@ __device__ __noinline__ int pick_near(const RouteArgs& p, const T* row, int lane
     }
   }
   if (n > 32) return n;
+  zero = __all_sync(kFull, zero);
   z = warp_sum(z);
   __syncwarp();
   const int c = lane < n ? cand->col[lane] : 0;
   const double l = (double)usable<T>(Elem<T>::to_f(row[c]));
   const double num = p.sigmoid ? 1.0 : exp(l - (double)m);
-  const double v = num / (p.sigmoid ? 1.0 + exp(-l) : z) + (p.bias ? (double)p.bias[c] : 0.0);
+  const double v = zero ? l : num / (p.sigmoid ? 1.0 + exp(-l) : z) + (p.bias ? (double)p.bias[c] : 0.0);
   cand->val[lane] = v;
   __syncwarp();
   int rank = 0;
@@ -523,7 +541,7 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const __grid_const
       float v[NC];  // pick_any takes its values by address: c stays in registers
 #pragma unroll
       for (int j = 0; j < NC; ++j) v[j] = c[j] == c[j] ? c[j] : -INFINITY;  // a NaN bias masks too
-      id = pick_any<float, NC>(v, p, lane, eps, &near_group);  // which of the two was close is not told
+      id = pick_any<T, float, NC>(v, nullptr, p, lane, eps, &near_group);  // which of the two was close is not told
     } else {
       uint32_t key[NC];
 #pragma unroll
