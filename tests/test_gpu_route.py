@@ -20,6 +20,7 @@ pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 HALF_STEP = {"f32": U, "bf16": 2.0 ** -8}
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+LOW = torch.finfo(torch.float32).min
 SCORE = {"sigmoid": moe.MOE_SCORE_SIGMOID, "softmax": moe.MOE_SCORE_SOFTMAX}
 
 
@@ -217,6 +218,28 @@ def test_biases_past_the_range_of_fp32(score, b, G, want):
         assert torch.equal(ids.cpu(), torch.tensor(want, dtype=torch.int32).expand(T, -1))
         share = torch.tensor([1.0 if i >= 0 else 0.0 for i in want])
         assert torch.allclose(w.cpu(), (share / share.sum()).expand(T, -1))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("masked,b,G,want", [
+    # sums of two of about -6.8e38 pass fp32's range, and still come before a group that is masked throughout
+    ([0, 1], [0.0, 0.0, LOW, LOW, LOW, LOW, 0.5, 0.5], 4, [6, 7, 2, 3]),
+    ([0, 1, 2], [0.0, 0.0, 0.0, LOW, LOW, LOW, 0.5, 0.5, 0.5], 3, [6, 7, 8, 3]),
+    # and differ among themselves: -5e38 before -6e38, -4e38 before both
+    ([], [-3e38, -3e38, -2e38, -3e38, -2e38, -2e38, -3e38, -3e38], 4, [2, 4, 5, 3]),
+    ([], [-3e38, -3e38, -3e38, -2e38, -3e38, -3e38, -2e38, -2e38, -3e38], 3, [3, 6, 7, 4]),
+])
+def test_group_sums_below_the_range_of_fp32(score, masked, b, G, want):
+    bias = torch.tensor(b, device="cuda")
+    for T in (1, 33, 8201):
+        l = torch.zeros(T, len(b), device="cuda")
+        l[:, masked] = float("-inf")
+        cfg = _cfg(l, len(want), score, G, 2, 2)
+        ids, w = _run(l, bias, cfg)
+        ref, _, _ = oracle.route_logits(_f64(l[:1]), _f64(bias), len(want), score, G, 2, 2)
+        assert ref[0].tolist() == want
+        assert torch.equal(ids.cpu(), torch.tensor(want, dtype=torch.int32).expand(T, -1))
+        assert torch.allclose(w, torch.full_like(w, 0.25))
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])

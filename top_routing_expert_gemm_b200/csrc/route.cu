@@ -154,10 +154,17 @@ __device__ __forceinline__ F neg_inf();
 template <> __device__ __forceinline__ float neg_inf<float>() { return -INFINITY; }
 template <> __device__ __forceinline__ double neg_inf<double>() { return -(double)INFINITY; }
 
+// A group's two largest choices added up.  In fp32 the sum stays above -inf,
+// which is a group without experts: sums of biases below the range meet at its
+// end, where they are close (the bound grows with the biases) and binary64 decides.
+__device__ __forceinline__ float sum_of_two(float a, float b) { return fmaxf(a + b, lowest<float>()); }
+__device__ __forceinline__ double sum_of_two(double a, double b) { return a + b; }
+
 // The picks of one row for any group shape, from the choices c (-inf: not to
 // be picked) of the warp's columns; the groups kept, the experts rank by them, or
-// by their logits (row, not null).  Lane s < k returns slot s (-1: none left).  near: two values whose order decides something were within eps
-// (group scores: 2 eps).  Used in fp32 where a group is no aligned run of
+// by their logits (row, not null).  Lane s < k returns slot s (-1: none left).
+// near: two values whose order decides something were within eps (group scores:
+// 2 eps).  Used in fp32 where a group is no aligned run of
 // lanes, and in binary64 for the rows whose fp32 decision was too close.
 template <typename T, typename F, int NC>
 __device__ __noinline__ int pick_any(F (&c)[NC], const T* row, const RouteArgs& p, int lane, F eps, bool* near) {
@@ -180,7 +187,7 @@ __device__ __noinline__ int pick_any(F (&c)[NC], const T* row, const RouteArgs& 
         b = fmax(fmin(a, oa), fmax(b, ob));
         a = fmax(a, oa);
       }
-      if (p.group_top == 2 && b > neg_inf<F>()) a += b;
+      if (p.group_top == 2 && b > neg_inf<F>()) a = sum_of_two(a, b);
       if (lane == g) mine = a;
     }
     int rank = 0;
@@ -560,7 +567,7 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const __grid_const
           a = max(a, oa);
         }
         uint32_t gk = a;
-        if (p.group_top == 2 && a2) gk = key_of(float_of(a) + float_of(a2));
+        if (p.group_top == 2 && a2) gk = key_of(sum_of_two(float_of(a), float_of(a2)));
         if (c0 >= p.E) gk = 0;
         const int mine = lane / lanes_g;
         int rank = 0;
@@ -870,7 +877,7 @@ __global__ void __launch_bounds__(kThreads) route_tile_kernel(const __grid_const
         a2 = fmaxf(fminf(a, bm[i]), fmaxf(a2, bm2[i]));
         a = fmaxf(a, bm[i]);
       }
-      score[g] = p.group_top == 2 && a2 > -INFINITY ? a + a2 : a;
+      score[g] = p.group_top == 2 && a2 > -INFINITY ? sum_of_two(a, a2) : a;
     }
     __syncwarp();
     kept = 0;
