@@ -405,8 +405,8 @@ moe_status moe_route_backward(const moe_route_config* cfg, const void* logits, c
      grad_y_perm[row_of[t*k+s]] = topk_w[t,s] * grad_y[t]     (dtype)
      grad_w[t,s] = <grad_y[t], y_perm[row_of[t*k+s]]>         (fp32; 0 for a dropped slot)
    Either output may be NULL (y_perm is only read for grad_w, topk_w only for
-   grad_y_perm; they may then be NULL too).  Rows that no slot points at are
-   left as they were.  The shared experts' gradient is grad_y itself.
+   grad_y_perm; they may then be NULL too).  grad_y_perm may be y_perm itself,
+   not grad_y.  Rows that no slot points at are left as they were.  The shared experts' gradient is grad_y itself.
    Deterministic.  Runs on the device of grad_y. */
 moe_status moe_combine_backward(const moe_config* cfg, const void* grad_y, const void* y_perm,
                                 const int32_t* row_of, const float* topk_w, void* grad_y_perm, float* grad_w,

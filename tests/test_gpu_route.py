@@ -461,6 +461,81 @@ def test_combine_backward_matches_the_oracle(dtype, T, d, E, k, cap):
     assert torch.equal(rows, rows2) and torch.equal(gw, gw2)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d,k", [(40003, 40, 2), (10007, 1032, 3)])
+def test_combine_backward_of_more_tokens_than_blocks_and_in_place(dtype, T, d, k):
+    """Blocks that take several tokens, against the formula in binary64 on the
+    GPU; and the experts' rows replaced by their gradients."""
+    _, _, _, _, row_of = _dispatch(T, 8, k, d, T * k // 9)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    gy = torch.randn(T, d, generator=gen, device="cuda").to(DT[dtype])
+    yp = torch.randn(T * k, d, generator=gen, device="cuda").to(DT[dtype])
+    w = torch.rand(T, k, generator=gen, device="cuda")
+    cfg = moe.make_config(T, d, 8, k, 8, moe.MOE_BF16 if dtype == "bf16" else moe.MOE_F32, moe.MOE_SOFTMAX_TOPK)
+    rows = torch.full((T * k, d), 5.5, dtype=DT[dtype], device="cuda")
+    gw = torch.full((T, k), float("nan"), device="cuda")
+    moe.moe_combine_backward(cfg, gy, yp, row_of, w, rows, gw)
+    slot = torch.nonzero(row_of >= 0)[:, 0]
+    row, g = row_of[slot].long(), gy[slot // k].double()
+    want = g * w.reshape(-1)[slot, None].double()
+    err = (rows[row].double() - want).abs()
+    assert (err <= (HALF_STEP[dtype] + 2 * U) * want.abs() + 1e-40).all()
+    free = torch.ones(T * k, dtype=torch.bool, device="cuda")
+    free[row] = False
+    assert free.any() and rows[free].eq(5.5).all()
+    y = yp[row].double()
+    want_w = torch.zeros(T * k, dtype=torch.float64, device="cuda")
+    bound = torch.zeros_like(want_w)
+    want_w[slot], bound[slot] = (g * y).sum(1), (g * y).abs().sum(1)
+    assert ((gw.reshape(-1).double() - want_w).abs() <= (d / 32 + 16) * U * bound).all()
+    gw2 = torch.empty_like(gw)
+    yp[free] = 5.5
+    moe.moe_combine_backward(cfg, gy, yp, row_of, w, yp, gw2)
+    assert torch.equal(yp, rows) and torch.equal(gw2, gw)
+
+
+def test_combine_backward_refuses_the_incoming_gradient_as_its_output():
+    """grad_y is read by tokens whose rows others write; y_perm's rows are each
+    read and written by one token."""
+    T, d = 37, 64
+    row_of = torch.randperm(T, generator=torch.Generator().manual_seed(1)).int().cuda()
+    gy, yp, w = torch.randn(T, d, device="cuda"), torch.randn(T, d, device="cuda"), torch.rand(T, 1, device="cuda")
+    cfg = moe.make_config(T, d, 4, 1, 8, moe.MOE_F32, moe.MOE_SOFTMAX_TOPK)
+    kept = gy.clone()
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_combine_backward(cfg, gy, yp, row_of, w, gy, torch.empty_like(w))
+    assert e.value.status == 1
+    torch.cuda.synchronize()
+    assert torch.equal(gy, kept)
+
+
+@pytest.mark.parametrize("score,renorm", [("sigmoid", 1), ("softmax", 0)])
+@pytest.mark.parametrize("E,k,dtype", [(24, 3, "f32"), (300, 5, "bf16")])
+def test_route_backward_of_more_rows_than_warps(score, renorm, E, k, dtype):
+    """Warps that take several rows: the gradients of the rows alone (whose
+    penalties are shares of a batch of their own)."""
+    few = _logits(53, E, dtype, E, 0.2, 3)
+    l = _repeated(few, 30011)
+    g = torch.randn(53, k, generator=torch.Generator().manual_seed(8)).cuda()
+    counts = torch.arange(1, E + 1, dtype=torch.int32, device="cuda")
+    out = []
+    for rows in (few, l):
+        T = rows.shape[0]
+        cfg = _cfg(rows, k, score, renorm=renorm, scale=1.5)
+        ids, _ = _run(rows, None, cfg)
+        grad = torch.full((T, E + 3), 77.0, dtype=rows.dtype, device="cuda")
+        moe.moe_route_backward(cfg, rows, ids, g.repeat(-(-T // 53), 1)[:T].contiguous(), counts, 0.5 * T / 53,
+                               0.25 * T / 53, grad[:, :E])
+        assert grad[:, E:].eq(77.0).all()
+        out.append(grad)
+    # the coefficients, T / 53 times as large over T rows, are the same up to roundings of the division
+    a, b = out[0].double(), out[1].double()[:53]
+    mag = 1.5 * g.abs().max() + 0.5 * E / 53 + 0.5 / 53 * 10
+    assert ((a - b).abs() <= 2 * HALF_STEP[dtype] * a.abs() + 8 * U * mag).all()
+    for at in range(53, 30011 - 53, 53 * 47):
+        assert torch.equal(out[1][at:at + 53], out[1][:53])
+
+
 # ------------------------------------------------------------------ together
 def test_router_gradient_through_the_layer():
     """route -> dispatch -> experts -> combine and back to the logits: the

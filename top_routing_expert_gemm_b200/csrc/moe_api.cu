@@ -506,6 +506,7 @@ moe_status moe_combine_backward(const moe_config* cfg, const void* grad_y, const
     return MOE_ERR_INVALID_ARG;
   DeviceGuard g;
   if ((st = enter(g, grad_y, stream)) != MOE_OK) return st;
+  if (grad_y_perm == grad_y) return MOE_ERR_INVALID_ARG;  // other tokens' rows would overwrite what a token reads
   CombineBackwardArgs a{grad_y, y_perm, row_of, topk_w, grad_y_perm, grad_w, cfg->T, cfg->top_k, cfg->d_model,
                         cfg->dtype == MOE_BF16};
   MOE_CUDA_TRY(launch_combine_backward(a, stream));
