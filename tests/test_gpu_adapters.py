@@ -241,6 +241,73 @@ def test_adapters_on_a_side_stream_and_captured():
     assert np.all(np.abs(_f64(out) - h) <= (2.0 ** -8 + 40 * U) * np.abs(h) + 1e-37)
 
 
+def test_captured_plan_of_several_chunks_replays_on_other_adapters():
+    """A captured plan of more than one chunk clears its header and its chunks'
+    states in every replay."""
+    c = Case(T=900, d=136, f=200, E=4, k=2, N=6, r=16, dtype="bf16").tensors("down")
+    want = []
+    first, second = c.ta.clone(), c.ta.roll(17)
+    for ta in (first, second):
+        c.ta = ta
+        c.out.fill_(5.5)
+        c.call("down", c.plan())
+        want.append(c.out.clone())
+    live, plan = first.clone(), c.plan()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_adapter_plan(c.cfg, c.ad, c.offsets, c.perm, live, plan)
+        c.call("down", plan)
+    for i in (0, 1, 1, 0):
+        live.copy_((first, second)[i])
+        c.out.fill_(5.5)
+        graph.replay()
+        assert moe.moe_device_status(plan) == 0
+        assert torch.equal(c.out, want[i])
+    live.fill_(c.N)  # every id past the end: reported, and treated as none
+    graph.replay()
+    assert moe.moe_device_status(plan) == moe.MOE_ERR_BAD_ADAPTER_ID
+    assert torch.equal(c.out[:c.live], c.base[:c.live])
+
+
+@pytest.mark.parametrize("E,N,shared", [(1024, 8191, False), (1, 65536, True)])
+def test_the_last_of_the_most_pairs(E, N, shared):
+    """The largest numbers of experts and adapters: keys up to 2^31, weights past
+    2^31 bytes apart.  Rows of the first and the last pair."""
+    T, d, r = 300, 16, 8
+    gen = torch.Generator(device="cuda").manual_seed(E)
+    cfg = moe.make_config(T, d, E, 1, d, moe.MOE_BF16, moe.MOE_SOFTMAX_TOPK, n_shared=int(shared),
+                          d_ff_shared=d if shared else 0)
+    ad = moe.make_adapter_config(N, r, int(shared))
+    plan = torch.empty(moe.moe_adapter_plan_bytes(cfg, ad), dtype=torch.uint8, device="cuda")
+    offsets = perm = None
+    expert = torch.zeros(T, dtype=torch.int64, device="cuda")
+    if not shared:
+        offsets = torch.full((E + 1,), 100, dtype=torch.int32, device="cuda")  # 100 rows of expert 0, 200 of the last
+        offsets[0], offsets[E] = 0, T
+        perm = torch.arange(T, dtype=torch.int32, device="cuda")
+        expert[100:] = E - 1
+    ta = torch.where(torch.arange(T, device="cuda") % 3 == 0, 0, N - 1).int()
+    a = torch.zeros(N, E, r, d, dtype=torch.bfloat16, device="cuda")
+    b = torch.zeros(N, E, d, r, dtype=torch.bfloat16, device="cuda")
+    for n in (0, N - 1):
+        for e in {0, E - 1}:
+            a[n, e] = torch.randn(r, d, generator=gen, device="cuda")
+            b[n, e] = torch.randn(d, r, generator=gen, device="cuda")
+    scale = torch.ones(N, device="cuda")
+    h, base = (torch.randn(T, d, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    y = torch.empty_like(base)
+    moe.moe_adapter_plan(cfg, ad, offsets, perm, ta, plan)
+    moe.moe_adapter_down(cfg, ad, plan, h, a, b, scale, base, y)
+    assert moe.moe_device_status(plan) == 0
+    A, B = a[ta.long(), expert].double(), b[ta.long(), expert].double()
+    u, mag = torch.einsum("trd,td->tr", A, h.double()), torch.einsum("trd,td->tr", A.abs(), h.abs().double())
+    want = base.double() + torch.einsum("tor,tr->to", B, u)
+    tol = torch.einsum("tor,tr->to", B.abs(), mag) * (64 * U + 2.0 ** -17) + (2.0 ** -8 + 4 * U) * want.abs()
+    assert ((y.double() - want).abs() <= tol).all()
+    del a, b, A, B
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_equal_calls_give_equal_results(dtype):
     """More chunks than one of rows, and tiles whose sums several blocks share."""
@@ -666,3 +733,52 @@ def test_layer_flags_bad_adapter_ids_and_replays():
     ta[7] = -1
     graph.replay()
     assert moe.moe_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("T,dtype,cap,n_shared", [(300, "bf16", 0.75, 1), (700, "f32", 0.5, 1), (1100, "bf16", 1.0, 0)])
+def test_layer_with_adapters_a_capacity_and_empty_slots(T, dtype, cap, n_shared):
+    """Everything that leaves a slot out at once: masked tokens, tokens with one
+    expert left, experts over their capacity, tokens without an adapter; the
+    reference walks the slots in token order, in binary64.  Tolerances of the test
+    above."""
+    E, k, d, f, N, r = 4, 2, 128, 96, 3, 16
+    cfg, route, t = _layer(T, d, f, E, k, dtype, n_shared, seed=T, cap=cap)
+    gen = torch.Generator().manual_seed(T)
+    t["logits"][:, 1] += 1.0  # a hot expert
+    t["logits"][(torch.rand(T, generator=gen) < 0.1).cuda()] = float("-inf")
+    t["logits"][:, 1:] = t["logits"][:, 1:].masked_fill((torch.rand(T, 1, generator=gen) < 0.1).cuda(), float("nan"))
+    routed, shared = _adapters(cfg, N, r, dtype, gen, n_shared)
+    ta = torch.randint(-1, N, (T,), generator=gen).int().cuda()
+    scale = torch.tensor([0.5, -1.0, 2.0], device="cuda")
+    y, ids, w, counts, ws = _forward(cfg, route, t, moe.make_adapters(N, r, ta, scale, *routed, *shared))
+    assert moe.moe_device_status(ws) == 0
+    C = moe.lib().moe_expert_capacity(cfg)
+    x, sc, idn, wn, tan = _f64(t["x"]), _f64(scale), ids.cpu().numpy(), _f64(w), ta.cpu().numpy()
+
+    def host(ts):
+        return [None if v is None else _f64(v) for v in ts]
+    r_w, s_w, (gu, dn, sgu, sdn) = host(routed), host(shared), host(t[n] for n in ("w_gu", "w_d", "s_gu", "s_d"))
+
+    def expert(xt, gu, dn, n, e, four):
+        v = gu @ xt
+        if n >= 0:
+            v = v + sc[n] * four[1][n, e] @ (four[0][n, e] @ xt)
+        h = oracle.silu(v[:f]) * v[f:]
+        o = dn @ h
+        return o + sc[n] * four[3][n, e] @ (four[2][n, e] @ h) if n >= 0 else o
+
+    want, seen, dropped = np.zeros((T, d)), np.zeros(E, np.int64), 0
+    for tok in range(T):
+        for s in range(k):
+            e = int(idn[tok, s])
+            if e < 0:
+                continue
+            seen[e] += 1
+            if seen[e] > C:
+                dropped += 1
+                continue
+            want[tok] += wn[tok, s] * expert(x[tok], gu[e], dn[e], tan[tok], e, r_w)
+        if n_shared:
+            want[tok] += expert(x[tok], sgu[0], sdn[0], tan[tok], 0, s_w)
+    assert dropped > 0 and (idn < 0).any() and np.array_equal(counts.cpu().numpy(), seen)
+    assert np.max(np.abs(_f64(y) - want)) <= {"f32": 1e-4, "bf16": 2e-2}[dtype] * np.max(np.abs(want))
