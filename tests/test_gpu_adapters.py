@@ -241,6 +241,16 @@ def test_adapters_on_a_side_stream_and_captured():
     assert np.all(np.abs(_f64(out) - h) <= (2.0 ** -8 + 40 * U) * np.abs(h) + 1e-37)
 
 
+@pytest.mark.parametrize("T", [70, 700])
+def test_plan_of_a_perm_that_ends_with_its_rows(T):
+    """A capacity leaves fewer rows than slots; perm may hold just those."""
+    c = Case(T=T, d=72, f=88, E=4, k=2, N=2, r=16, dtype="bf16", cap=T // 4).tensors("down")
+    assert c.live < c.rows
+    c.perm = c.perm[:c.live].clone()
+    c.call("down", c.plan())
+    c.check("down")
+
+
 def test_captured_plan_of_several_chunks_replays_on_other_adapters():
     """A captured plan of more than one chunk clears its header and its chunks'
     states in every replay."""

@@ -141,20 +141,17 @@ __global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanPa
   const bool alone = gridDim.x == 1;
   if (!alone && tid == 0) s_chunk = atomicAdd(p.turn, 1);
   bool bad = false;
-  // the row's slot (garbage behind the last row: not used there)
-  int slot = alone && p.perm && tid < kChunkRows && tid < p.rows ? p.perm[tid] : 0;
   if (p.offsets)
     for (int e = tid; e <= p.E; e += kPlanThreads) s_off[e] = p.offsets[e];
   __syncthreads();
   const int chunk = alone ? 0 : s_chunk;
   const int64_t row0 = (int64_t)chunk * kChunkRows;
   const int64_t row = row0 + tid;
-  if (!alone && p.perm && tid < kChunkRows && row < p.rows) slot = p.perm[row];
   const int64_t live = p.offsets ? min((int64_t)s_off[p.E], p.rows) : p.rows;
   if (tid < kChunkRows) {
     int pair = kSkip;
     if (row < live) {
-      int a = p.token_adapter[p.perm ? slot / p.k : row];
+      int a = p.token_adapter[p.perm ? p.perm[row] / p.k : row];
       if (a >= p.N) {
         bad = true;
         a = -1;
