@@ -310,13 +310,15 @@ __device__ __forceinline__ Parts parts_of(int tile, int n_tiles, int units, int 
   const int64_t total = (int64_t)n_tiles * units, at = (int64_t)tile * units;
   return Parts{block_of(at, total, blocks), block_of(at + units - 1, total, blocks)};
 }
-// U[i, k..k+3] of a tile, all partial sums
+// U[i, k..k+3] of a tile, all partial sums.  Ordinary loads: the shrink may still
+// write them when this kernel starts (pdl.cuh), and the read-only path is for
+// what nobody writes as long as a kernel lives.
 __device__ __forceinline__ float4 sum_parts(const float* u, const float* more, int start, Parts parts, int r,
                                             int i, int k) {
-  float4 v = __ldg(reinterpret_cast<const float4*>(u + (int64_t)(start + i) * r + k));
+  float4 v = *reinterpret_cast<const float4*>(u + (int64_t)(start + i) * r + k);
 #pragma unroll 4
   for (int b = parts.first + 1; b <= parts.last; ++b) {
-    const float4 w = __ldg(reinterpret_cast<const float4*>(more + ((int64_t)b * kTileRows + i) * r + k));
+    const float4 w = *reinterpret_cast<const float4*>(more + ((int64_t)b * kTileRows + i) * r + k);
     v.x += w.x;
     v.y += w.y;
     v.z += w.z;
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(kThreads) adapter_shrink_f32_kernel(const Shri
       for (int k = k_lo + 4 * lane; k < k_hi; k += 128) {
         float4 xv[4], av[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) xv[i] = __ldg(reinterpret_cast<const float4*>(xr[i] + k));
+        for (int i = 0; i < 4; ++i) xv[i] = *reinterpret_cast<const float4*>(xr[i] + k);
 #pragma unroll
         for (int c = 0; c < 8; ++c) av[c] = __ldg(reinterpret_cast<const float4*>(a + (int64_t)(c0 + c) * p.K + k));
 #pragma unroll
