@@ -792,3 +792,43 @@ def test_layer_with_adapters_a_capacity_and_empty_slots(T, dtype, cap, n_shared)
             want[tok] += expert(x[tok], sgu[0], sdn[0], tan[tok], 0, s_w)
     assert dropped > 0 and (idn < 0).any() and np.array_equal(counts.cpu().numpy(), seen)
     assert np.max(np.abs(_f64(y) - want)) <= {"f32": 1e-4, "bf16": 2e-2}[dtype] * np.max(np.abs(want))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,d,f,E,k,act", [
+    (2048, 2880, 2880, 16, 4, "swiglu"), (20, 4096, 3584, 8, 2, "swiglu"), (600, 1024, 1040, 4, 2, "gelu"),
+    (1, 2048, 1408, 16, 4, "swiglu"), (3000, 512, 5776, 2, 1, "swiglu")])
+def test_layer_of_real_widths_with_adapters_that_add_nothing(T, d, f, E, k, act, e4m3):
+    """First products without their activation, at widths of many column tiles,
+    under the batch and the decode GEMMs: with adapters of weight zero (B = 0) the
+    layer is the one without adapters, but for the pre-activations' rounding to
+    bf16 (and, with 8-bit experts, the codes of h that it moves).  Tolerances of
+    the tests above; a misplaced column would be off by the outputs' own size."""
+    N, r = 2, 16
+    m = 2 if act == "swiglu" else 1
+    gen = torch.Generator(device="cuda").manual_seed(T)
+
+    def randn(*s, std=1.0):
+        return torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_(0.0, std, generator=gen)
+    t = dict(x=randn(T, d), logits=torch.randn(T, E, generator=gen, device="cuda"), w_gu=randn(E, m * f, d, std=d ** -0.5),
+             w_d=randn(E, d, f, std=f ** -0.5), s_gu=None, s_d=None)
+    cfg = moe.make_config(T, d, E, k, f, moe.MOE_BF16, moe.MOE_SOFTMAX_TOPK,
+                          expert_act=moe.MOE_ACT_SWIGLU if act == "swiglu" else moe.MOE_ACT_GELU,
+                          weight_format=moe.MOE_W_E4M3 if e4m3 else moe.MOE_W_NATIVE)
+    route = moe.make_route_config(T, E, k, moe.MOE_SCORE_SOFTMAX)
+    if e4m3:
+        t["w_gu"], t["w_d"] = _blob(t["w_gu"]), _blob(t["w_d"])
+    a1, b1 = randn(N, E, r, d), torch.zeros(N, E, m * f, r, dtype=torch.bfloat16, device="cuda")
+    a2, b2 = randn(N, E, r, f), torch.zeros(N, E, d, r, dtype=torch.bfloat16, device="cuda")
+    ta = (torch.arange(T, device="cuda") % 3 - 1).int()
+    scale = torch.ones(N, device="cuda")
+    want, ids, _, _, ws = _forward(cfg, route, t)
+    assert moe.moe_device_status(ws) == 0
+    for parts in ((a1, b1, a2, b2), (a1, b1, None, None), (None, None, a2, b2)):
+        y, ids2, _, _, ws = _forward(cfg, route, t, moe.make_adapters(N, r, ta, scale, *parts))
+        assert moe.moe_device_status(ws) == 0
+        assert torch.equal(ids, ids2)
+        if parts[0] is None:
+            assert torch.equal(y, want)
+        tol = 4e-2 if e4m3 else 2e-2
+        assert float((y.float() - want.float()).abs().max()) <= tol * float(want.float().abs().max())
