@@ -360,6 +360,30 @@ def test_route_backward_counts_of_zero_and_empty_terms():
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("z", [0.0, 0.25])
+def test_masked_experts_have_no_gradient_whatever_the_incoming_one_is(score, renorm, z):
+    """An incoming gradient that is infinite or NaN stays in its row and out of the
+    masked columns, and at a slot on a masked expert it is not used at all."""
+    inf, nan = float("inf"), float("nan")
+    l = torch.randn(6, 40, generator=torch.Generator().manual_seed(12)).cuda()
+    l[:, 3], l[:, 20] = -inf, torch.finfo(torch.float32).min
+    ids = torch.tensor([[0, 5, 39], [1, 2, 4], [3, 7, 8], [20, 3, 9], [6, 7, 8], [5, 6, 7]], dtype=torch.int32).cuda()
+    g = torch.randn(6, 3, generator=torch.Generator().manual_seed(13)).cuda()
+    g[1, 1], g[4, 0] = inf, nan                 # on picks that count
+    g[2, 0], g[3, 0], g[3, 1] = nan, inf, nan   # on masked experts
+    cfg = _cfg(l, 3, score, renorm=renorm)
+    grad = torch.full_like(l, 77.0)
+    moe.moe_route_backward(cfg, l, ids, g, None, 0.0, z, grad)
+    torch.cuda.synchronize()
+    assert grad[:, 3].eq(0).all() and grad[:, 20].eq(0).all()
+    rows = [0, 2, 3, 5]
+    _grad_check(l[rows], ids[rows], torch.nan_to_num(g[rows], posinf=0.0), _cfg(l[rows], 3, score, renorm=renorm), score,
+                None, 0.0, z * 4 / 6, "f32", grad[rows])  # the penalty is a mean over 6 rows
+    assert not grad[1].isfinite().all() and not grad[4].isfinite().all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [0, 1])
 @pytest.mark.parametrize("balance,z", [(0.0, 0.0), (0.5, 0.25)])
 def test_gradients_of_repeated_and_stray_ids_match_the_oracle(score, renorm, balance, z):
     """Every slot of a repeated id counts with its own gradient, a stray id is an

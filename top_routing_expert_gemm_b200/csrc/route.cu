@@ -1063,11 +1063,11 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks<NC>) route_backward_
   for (; t < p.T; t += step) {
     const T* row = logits + t * p.stride;
     const int id = nid >= 0 && nid < p.E ? nid : -1;
-    const float g = id >= 0 ? ng : 0.f;
     float v[NC];
 #pragma unroll
     for (int j = 0; j < NC; ++j) v[j] = dense ? usable<T>(nv[j]) : 0.f;
     const float l = id >= 0 ? usable<T>(Elem<T>::to_f(row[id])) : -INFINITY;
+    const float g = l > -INFINITY ? ng : 0.f;  // whatever it is at an empty slot or a masked expert
     if (t + step < p.T) fetch(t + step);
 
     // ---- maxima of the row and of the picks, then all sums in one pass
@@ -1112,12 +1112,13 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks<NC>) route_backward_
       } else {
         part = q * rest * g;
       }
+      part = l > -INFINITY ? part : 0.f;  // also where the other slots' sums are infinite or NaN
     }
     if (dense) {
       if (p.z != 0.f && z > 0.f) shared += cz * (m + logf(z));
       const float mean = fp * inv;
 #pragma unroll
-      for (int j = 0; j < NC; ++j) v[j] = v[j] * inv * fmaf(cb, f[j] - mean, shared);
+      for (int j = 0; j < NC; ++j) v[j] = v[j] > 0.f ? v[j] * inv * fmaf(cb, f[j] - mean, shared) : 0.f;
     }
     if (p.grad_w) {
       // the picks' parts join the row in shared memory, repeated ids one after the other
