@@ -241,6 +241,24 @@ def test_adapters_on_a_side_stream_and_captured():
     assert np.all(np.abs(_f64(out) - h) <= (2.0 ** -8 + 40 * U) * np.abs(h) + 1e-37)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("which", ["gate_up", "down"])
+def test_what_no_row_uses_is_not_used(which, dtype):
+    """NaN in the inputs of rows without an adapter and in the weights and scales
+    of adapters that no token has."""
+    c = Case(T=300, d=136, f=200, E=4, k=2, N=6, r=24, dtype=dtype).tensors(which)
+    c.ta[c.ta == 2] = -1
+    c.adapter = np.where(c.adapter == 2, -1, c.adapter)
+    c.call(which, c.plan())
+    want = c.out.clone()
+    c.a[2], c.b[2], c.scale[2] = float("nan"), float("inf"), float("nan")
+    c.x[:c.live][torch.from_numpy(c.adapter < 0).cuda()] = float("nan")
+    c.out.fill_(5.5)
+    c.call(which, c.plan())
+    assert (c.adapter < 0).any() and torch.equal(c.out, want)
+    assert c.out[:c.live].isfinite().all()
+
+
 @pytest.mark.parametrize("T", [70, 700])
 def test_plan_of_a_perm_that_ends_with_its_rows(T):
     """A capacity leaves fewer rows than slots; perm may hold just those."""
