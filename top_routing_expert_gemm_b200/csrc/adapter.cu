@@ -85,8 +85,9 @@ constexpr int kPlanThreads = 4 * kChunkRows;
 
 // The tiles stand in the order of the chunks, so that equal calls cut them into
 // equal runs and give equal results.  A chunk's place is the number of tiles
-// before it: every block publishes its own number, and its first warp adds up
-// those before it, 32 at a time, down to one that has published its total.
+// before it (a scan with decoupled look-back): every block publishes its own
+// number, and its first warp adds up those before it, 32 at a time, down to one
+// that has published its total.
 // Blocks take their chunks in turn, so whoever waits waits for running blocks.
 // (Places from one atomic counter took 6.3 us against 8 for 16 chunks and 7 against
 // 12 for 128, but then the order of the tiles, and with it the last bits of U,
@@ -1091,20 +1092,20 @@ cudaError_t allow_smem(K kernel, int smem) {
 }
 
 template <int RT>
-cudaError_t run_shrink(const ShrinkParams& p, dim3 grid, bool chained, cudaStream_t stream) {
+cudaError_t run_shrink(const ShrinkParams& p, dim3 grid, cudaStream_t stream) {
   const cudaError_t e = allow_smem(adapter_shrink_kernel<RT>, shrink_smem<RT>());
   if (e != cudaSuccess) return e;
-  return launch_maybe_chained(adapter_shrink_kernel<RT>, grid, dim3(kThreads), shrink_smem<RT>(), stream, chained, p);
+  return launch_maybe_chained(adapter_shrink_kernel<RT>, grid, dim3(kThreads), shrink_smem<RT>(), stream, true, p);
 }
 
-cudaError_t launch_shrink(const ShrinkParams& p, bool bf16, dim3 grid, bool chained, cudaStream_t stream) {
+cudaError_t launch_shrink(const ShrinkParams& p, bool bf16, dim3 grid, cudaStream_t stream) {
   if (!bf16)
-    return launch_maybe_chained(adapter_shrink_f32_kernel, grid, dim3(kThreads), 0, stream, chained, p);
-  if (p.r <= 8) return run_shrink<1>(p, grid, chained, stream);
-  if (p.r <= 16) return run_shrink<2>(p, grid, chained, stream);
-  if (p.r <= 32) return run_shrink<4>(p, grid, chained, stream);
-  if (p.r <= 64) return run_shrink<8>(p, grid, chained, stream);
-  return run_shrink<16>(p, grid, chained, stream);
+    return launch_maybe_chained(adapter_shrink_f32_kernel, grid, dim3(kThreads), 0, stream, true, p);
+  if (p.r <= 8) return run_shrink<1>(p, grid, stream);
+  if (p.r <= 16) return run_shrink<2>(p, grid, stream);
+  if (p.r <= 32) return run_shrink<4>(p, grid, stream);
+  if (p.r <= 64) return run_shrink<8>(p, grid, stream);
+  return run_shrink<16>(p, grid, stream);
 }
 
 // As many blocks per SM as leave each a ring of two stages
@@ -1150,7 +1151,7 @@ size_t adapter_plan_bytes(const AdapterShape& s) { return layout(s).total; }
 
 cudaError_t launch_adapter_plan(const AdapterShape& s, const int32_t* offsets, const int32_t* perm,
                                 const int32_t* token_adapter, void* plan, int* status, uint64_t wait_limit_ns,
-                                bool chained, cudaStream_t stream) {
+                                cudaStream_t stream) {
   uint8_t* base = static_cast<uint8_t*>(plan);
   const PlanLayout l = layout(s);
   if (s.rows == 0) return cudaSuccess;
@@ -1159,14 +1160,14 @@ cudaError_t launch_adapter_plan(const AdapterShape& s, const int32_t* offsets, c
                reinterpret_cast<int2*>(base + kAdapterTilesAt), reinterpret_cast<int*>(base + kAdapterTurnAt),
                reinterpret_cast<unsigned long long*>(base + l.state), status, wait_limit_ns, blocks == 1 && status == plan};
   return launch_maybe_chained(adapter_plan_kernel, dim3(blocks), dim3(kPlanThreads), sizeof(int) * (size_t)(s.E + 1),
-                              stream, chained, p);
+                              stream, true, p);
 }
 
 size_t adapter_plan_clear_bytes(const AdapterShape& s) {
   return s.rows == 0 ? kAdapterHeader : s.rows > kChunkRows ? layout(s).tiles : 0;
 }
 
-cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, bool chained, cudaStream_t stream) {
+cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, cudaStream_t stream) {
   if (s.rows == 0) return cudaSuccess;
   uint8_t* base = static_cast<uint8_t*>(a.plan);
   const PlanLayout l = layout(s);
@@ -1179,12 +1180,12 @@ cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, b
   float* more = reinterpret_cast<float*>(base + l.more);
   const int blocks = shrink_blocks(s), units = (K + kUnitInputs - 1) / kUnitInputs;
   ShrinkParams sp{a.x, a.a, tiles, n_tiles, u, more, K, s.r, s.E};
-  cudaError_t e = launch_shrink(sp, s.bf16, dim3((unsigned)blocks), chained, stream);
+  cudaError_t e = launch_shrink(sp, s.bf16, dim3((unsigned)blocks), stream);
   if (e != cudaSuccess) return e;
   // fp32: one round of the block's threads, more where there are enough tiles to fill the SMs
   const int64_t guess = tiles_guess(s);
   const int64_t rounds = (n_res + kThreads - 1) / kThreads;
-  const int64_t per = std::max<int64_t>(1, std::min<int64_t>(rounds, rounds * guess / (148 * 8)));
+  const int64_t per = std::max<int64_t>(1, std::min<int64_t>(rounds, rounds * guess / (device_sm_count() * 8)));
   const int col_block = (int)std::min<int64_t>(per, 16) * kThreads;
   ExpandParams ep{u, more, a.b, a.scale, a.base, a.out, tiles, n_tiles, s.rows, s.r, s.E, units, blocks, n_out, n_res,
                   col_block, !a.gate_up && a.base == a.out, 0, 0, a.status, a.wait_limit_ns};

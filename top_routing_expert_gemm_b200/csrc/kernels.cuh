@@ -170,7 +170,7 @@ struct RouteBackwardArgs {
 };
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t stream);
 
-// ---- low-rank adapters beside the experts' projections (adapter.cu)
+// ---- low-rank adapters beside the experts' projections (adapter.cu); every launch is chained (pdl.cuh)
 struct AdapterShape {
   int64_t T, rows;        // tokens; dispatched rows (T*k, or T beside a shared expert)
   int d, f;               // inputs of the two projections
@@ -203,8 +203,8 @@ size_t adapter_plan_bytes(const AdapterShape& s);
 size_t adapter_plan_clear_bytes(const AdapterShape& s);
 cudaError_t launch_adapter_plan(const AdapterShape& s, const int32_t* offsets, const int32_t* perm,
                                 const int32_t* token_adapter, void* plan, int* status, uint64_t wait_limit_ns,
-                                bool chained, cudaStream_t stream);
-cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, bool chained, cudaStream_t stream);
+                                cudaStream_t stream);
+cudaError_t launch_adapter_apply(const AdapterShape& s, const AdapterApply& a, cudaStream_t stream);
 
 int device_sm_count();
 int device_smem_per_block();  // opt-in dynamic shared memory per block (227 KiB on B200)

@@ -269,7 +269,7 @@ moe_status adapter_apply(const moe_config* cfg, const moe_adapter_config* ad, bo
   if ((st = enter(g, plan, stream)) != MOE_OK) return st;
   if ((st = g.same_device(out)) != MOE_OK) return st;
   MOE_CUDA_TRY(launch_adapter_apply(s, AdapterApply{gate_up, x, a, b, scale, base, out, plan, static_cast<int*>(plan),
-                                                   wait_limit(cfg)}, true, stream));
+                                                   wait_limit(cfg)}, stream));
   return MOE_OK;
 }
 
@@ -339,18 +339,18 @@ cudaError_t run_adapted_ffn(const moe_config* c, const Carve& k, const moe_adapt
   const void* b1 = shared ? ad->b_gate_up_shared : ad->b_gate_up;
   const void* a2 = shared ? ad->a_down_shared : ad->a_down;
   const void* b2 = shared ? ad->b_down_shared : ad->b_down;
-  cudaError_t e = launch_adapter_plan(sh, offsets, perm, ad->token_adapter, plan, k.status, wait_limit(c), true, s);
+  cudaError_t e = launch_adapter_plan(sh, offsets, perm, ad->token_adapter, plan, k.status, wait_limit(c), s);
   if (e != cudaSuccess) return e;
   e = run_ffn(c, k, x, offsets, G, rows, f, w_gu, w_d, a1 ? pre : h, y, s, shared, a_quantized, true,
               a1 ? kFfnGemm1Plain : kFfnGemm1);
   if (e != cudaSuccess) return e;
   if (a1) {
-    e = launch_adapter_apply(sh, AdapterApply{true, x, a1, b1, ad->scale, pre, h, plan, k.status, wait_limit(c)}, true, s);
+    e = launch_adapter_apply(sh, AdapterApply{true, x, a1, b1, ad->scale, pre, h, plan, k.status, wait_limit(c)}, s);
     if (e != cudaSuccess) return e;
   }
   e = run_ffn(c, k, x, offsets, G, rows, f, w_gu, w_d, h, y, s, shared, true, true, kFfnGemm2);
   if (e != cudaSuccess || !a2) return e;
-  return launch_adapter_apply(sh, AdapterApply{false, h, a2, b2, ad->scale, y, y, plan, k.status, wait_limit(c)}, true, s);
+  return launch_adapter_apply(sh, AdapterApply{false, h, a2, b2, ad->scale, y, y, plan, k.status, wait_limit(c)}, s);
 }
 
 }  // namespace
@@ -648,8 +648,7 @@ moe_status moe_adapter_plan(const moe_config* cfg, const moe_adapter_config* ad,
   if ((st = enter(g, plan, stream)) != MOE_OK) return st;
   const size_t clear = adapter_plan_clear_bytes(s);
   if (clear) MOE_CUDA_TRY(cudaMemsetAsync(plan, 0, clear, stream));
-  MOE_CUDA_TRY(launch_adapter_plan(s, offsets, perm, token_adapter, plan, static_cast<int*>(plan), wait_limit(cfg), true,
-                                   stream));
+  MOE_CUDA_TRY(launch_adapter_plan(s, offsets, perm, token_adapter, plan, static_cast<int*>(plan), wait_limit(cfg), stream));
   return MOE_OK;
 }
 

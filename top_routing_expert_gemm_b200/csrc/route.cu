@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const __grid_const
     if (!by_logit || (p.G > 1 && !runs)) l = id >= 0 ? usable<T>(Elem<T>::to_f(row[id])) : -INFINITY;
     const float top = p.renorm ? warp_max(l) : 0.f;
     float zw = z;
-    if (!p.sigmoid && !p.renorm) {  // probabilities as they are: the denominator with expf
+    if (!p.sigmoid && !p.renorm) {  // probabilities as they are: the denominator with exp_near
       zw = 0.f;
       float lr[NC];
       load_cols<T, NC>(row, c0, p.E, p.vec, lr);
