@@ -162,18 +162,19 @@ __device__ __forceinline__ double sum_of_two(double a, double b) { return a + b;
 
 // The picks of one row for any group shape, from the choices c (-inf: not to
 // be picked) of the warp's columns; the groups kept, the experts rank by them, or
-// by their logits (row, not null).  Lane s < k returns slot s (-1: none left).
-// near: two values whose order decides something were within eps (group scores:
-// 2 eps).  Used in fp32 where a group is no aligned run of
-// lanes, and in binary64 for the rows whose fp32 decision was too close.
+// by their logits (row, not null).  G: the groups, 1 if they are chosen already.
+// Lane s < k returns slot s (-1: none left).  near: two values whose order decides
+// something were within eps (group scores: 2 eps).  Used in fp32 where a group is
+// no aligned run of lanes, and in binary64 for the rows whose fp32 decision was
+// too close.
 template <typename T, typename F, int NC>
-__device__ __noinline__ int pick_any(F (&c)[NC], const T* row, const RouteArgs& p, int lane, F eps, bool* near) {
+__device__ __noinline__ int pick_any(F (&c)[NC], const T* row, int G, const RouteArgs& p, int lane, F eps, bool* near) {
   bool close = false;
   const int c0 = lane * NC;
-  if (p.G > 1) {
-    const int gs = p.E / p.G;
+  if (G > 1) {
+    const int gs = p.E / G;
     F mine = neg_inf<F>();  // lane g: the score of group g
-    for (int g = 0; g < p.G; ++g) {
+    for (int g = 0; g < G; ++g) {
       F a = neg_inf<F>(), b = neg_inf<F>();
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
@@ -191,12 +192,12 @@ __device__ __noinline__ int pick_any(F (&c)[NC], const T* row, const RouteArgs& 
       if (lane == g) mine = a;
     }
     int rank = 0;
-    for (int g = 0; g < p.G; ++g) {
+    for (int g = 0; g < G; ++g) {
       const F o = __shfl_sync(kFull, mine, g);
       rank += o > mine || (o == mine && g < lane);
     }
-    const unsigned kept = __ballot_sync(kFull, lane < p.G && rank < p.Gk);
-    F lo = lane < p.G && rank < p.Gk ? mine : (F)INFINITY, hi = lane < p.G && rank >= p.Gk ? mine : neg_inf<F>();
+    const unsigned kept = __ballot_sync(kFull, lane < G && rank < p.Gk);
+    F lo = lane < G && rank < p.Gk ? mine : (F)INFINITY, hi = lane < G && rank >= p.Gk ? mine : neg_inf<F>();
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       lo = fmin(lo, __shfl_xor_sync(kFull, lo, off));
@@ -306,6 +307,16 @@ __device__ __forceinline__ int pick_candidates(const uint32_t (&key)[NC], const 
   return n;
 }
 
+// No bias, or zeros
+__device__ __forceinline__ bool no_bias(const RouteArgs& p, int lane) {
+  bool zero = true;
+  if (p.bias) {
+#pragma unroll 1
+    for (int c = lane; c < p.E; c += 32) zero &= p.bias[c] == 0.f;
+  }
+  return __all_sync(kFull, zero);
+}
+
 // The row again in binary64: scores from the fp32 or bf16 logits as stored.
 // runs: groups are aligned runs of lanes_g lanes.  Without a bias, or with zeros
 // (and groups by sums of two, or nothing would be close), the groups kept, the
@@ -315,15 +326,12 @@ __device__ __noinline__ int pick_exact(const RouteArgs& p, const T* row, int lan
                                        Picks<double>* cand, Picks<double>* order) {
   const int c0 = lane * NC;
   double c[NC];
-  bool zero = true;
   double m = -(double)INFINITY;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     c[j] = c0 + j < p.E ? (double)usable<T>(Elem<T>::to_f(row[c0 + j])) : -(double)INFINITY;
     m = fmax(m, c[j]);
-    zero &= !p.bias || c0 + j >= p.E || p.bias[c0 + j] == 0.f;
   }
-  zero = __all_sync(kFull, zero);
   double z = 0.0;
   if (!p.sigmoid) {
 #pragma unroll
@@ -361,17 +369,15 @@ __device__ __noinline__ int pick_exact(const RouteArgs& p, const T* row, int lan
       }
       kept = c0 < p.E && rank < p.Gk;
     }
+    const bool zero = no_bias(p, lane);
     uint32_t key[NC];
-    double by[NC];
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const bool in = kept && c[j] > -(double)INFINITY;
-      double v = c[j];
-      if (in && zero) v = (double)usable<T>(Elem<T>::to_f(row[c0 + j]));
-      key[j] = in ? key_of(fmaxf((float)v, lowest<float>())) : 0u;
-      by[j] = v;
+      if (!kept) c[j] = -(double)INFINITY;
+      if (zero && c[j] > -(double)INFINITY) c[j] = (double)usable<T>(Elem<T>::to_f(row[c0 + j]));
+      key[j] = c[j] > -(double)INFINITY ? key_of(fmaxf((float)c[j], lowest<float>())) : 0u;
     }
-    const int n = pick_candidates<double, NC>(key, by, p.k, c0, lane, cand, order);
+    const int n = pick_candidates<double, NC>(key, c, p.k, c0, lane, cand, order);
     if (n <= 32) {
       const int id = lane < min(n, p.k) ? order->col[lane] : -1;
       __syncwarp();
@@ -379,7 +385,8 @@ __device__ __noinline__ int pick_exact(const RouteArgs& p, const T* row, int lan
     }
   }
   bool unused;
-  return pick_any<T, double, NC>(c, zero ? row : nullptr, p, lane, 0.0, &unused);
+  const bool chosen = p.G == 1 || runs;
+  return pick_any<T, double, NC>(c, !chosen && no_bias(p, lane) ? row : nullptr, chosen ? 1 : p.G, p, lane, 0.0, &unused);
 }
 
 // The picks of a row whose kept groups are certain but whose order is not: only
@@ -395,7 +402,6 @@ __device__ __noinline__ int pick_near(const RouteArgs& p, const T* row, int lane
   const int gs = p.E / p.G;
   int n = 0;
   double z = 0.0;
-  bool zero = true;
 #pragma unroll 1
   for (int c0 = 0; c0 < p.E; c0 += 256) {  // 256 columns' loads in flight: the row is in L2 at best
     float l[8], b[8];
@@ -408,7 +414,6 @@ __device__ __noinline__ int pick_near(const RouteArgs& p, const T* row, int lane
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = c0 + 32 * j + lane;
-      zero &= b[j] == 0.f;
       const float v = (p.sigmoid ? sigmoid_fast(l[j]) : __expf(l[j] - m) * inv) + b[j];
       const bool in = l[j] > -INFINITY && v > -INFINITY && v >= thr && (p.G == 1 || kept >> (c / gs) & 1u);
       const unsigned who = __ballot_sync(kFull, in);
@@ -426,7 +431,7 @@ __device__ __noinline__ int pick_near(const RouteArgs& p, const T* row, int lane
     }
   }
   if (n > 32) return n;
-  zero = __all_sync(kFull, zero);
+  const bool zero = no_bias(p, lane);
   z = warp_sum(z);
   __syncwarp();
   const int c = lane < n ? cand->col[lane] : 0;
@@ -548,7 +553,7 @@ __global__ void __launch_bounds__(kThreads) route_topk_kernel(const __grid_const
       float v[NC];  // pick_any takes its values by address: c stays in registers
 #pragma unroll
       for (int j = 0; j < NC; ++j) v[j] = c[j] == c[j] ? c[j] : -INFINITY;  // a NaN bias masks too
-      id = pick_any<T, float, NC>(v, nullptr, p, lane, eps, &near_group);  // which of the two was close is not told
+      id = pick_any<T, float, NC>(v, nullptr, p.G, p, lane, eps, &near_group);  // which of the two was close is not told
     } else {
       uint32_t key[NC];
 #pragma unroll
@@ -718,7 +723,10 @@ __device__ __forceinline__ float quad_max(float v) {
   return fmaxf(v, __shfl_xor_sync(kFull, v, 2));
 }
 
-template <typename T, int NC>
+// BY_LOGIT: no bias and no sums over a group's two best, known at the launch, so
+// no row is close and the calls that decide those are not in the kernel: 65536
+// rows of 128, bf16, softmax: 13.3 against 17.0 us.
+template <typename T, int NC, bool BY_LOGIT>
 __global__ void __launch_bounds__(kThreads) route_tile_kernel(const __grid_constant__ RouteArgs p) {
   constexpr int NB = kTileBlocks<NC>;
   extern __shared__ __align__(16) float sm[];
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(kThreads) route_tile_kernel(const __grid_const
   // ---- the bias: in shared memory, zero throughout?, and its largest
   float bmax = 0.f;
   bool zero = true;
-  if (p.bias) {
+  if (!BY_LOGIT && p.bias) {
     for (int i = threadIdx.x; i < 16 * sh.nb; i += kThreads) {
       const int b = i / 16, j = i % 16, at = b % sh.nbg * sh.bl + j;
       const float v = j < sh.bl && at < sh.gs ? p.bias[b / sh.nbg * sh.gs + at] : 0.f;
@@ -751,9 +759,9 @@ __global__ void __launch_bounds__(kThreads) route_tile_kernel(const __grid_const
     }
     zero = __syncthreads_and(zero);
   }
-  const bool by_logit = zero && (p.G == 1 || p.group_top == 1);
+  const bool by_logit = BY_LOGIT || (zero && (p.G == 1 || p.group_top == 1));
   const bool need_z = !p.sigmoid && (!by_logit || !p.renorm);
-  if (!zero) {
+  if (!BY_LOGIT && !zero) {
     bmax = warp_max(bmax);
     float* part = reinterpret_cast<float*>(exact - threadIdx.x / 32 * 2);
     if (lane == 0) part[threadIdx.x / 32] = bmax;
@@ -805,7 +813,7 @@ __global__ void __launch_bounds__(kThreads) route_tile_kernel(const __grid_const
                                 : 0x1p-17f * inv + 0x1p-22f * (bmax + 1.0f * inv);
 
   // ---- choices and block maxima; four blocks are loaded at a time
-  const bool seconds = p.G > 1 && p.group_top == 2;
+  const bool seconds = !BY_LOGIT && p.G > 1 && p.group_top == 2;
   float top[NB];
   constexpr int NL = NB < 4 ? NB : 4;
 #pragma unroll
@@ -877,7 +885,7 @@ __global__ void __launch_bounds__(kThreads) route_tile_kernel(const __grid_const
         a2 = fmaxf(fminf(a, bm[i]), fmaxf(a2, bm2[i]));
         a = fmaxf(a, bm[i]);
       }
-      score[g] = p.group_top == 2 && a2 > -INFINITY ? sum_of_two(a, a2) : a;
+      score[g] = seconds && a2 > -INFINITY ? sum_of_two(a, a2) : a;
     }
     __syncwarp();
     kept = 0;
@@ -952,7 +960,7 @@ __global__ void __launch_bounds__(kThreads) route_tile_kernel(const __grid_const
     if (ids[s] >= 0) ids[s] = ids[s] / 16 / sh.nbg * sh.gs + ids[s] / 16 % sh.nbg * sh.bl + ids[s] % 16;
   __syncwarp();
   // rows that fp32 could not decide: the warp takes them one by one
-  if (__any_sync(kFull, (near || near_group) && live)) {
+  if (!BY_LOGIT && __any_sync(kFull, (near || near_group) && live)) {
     const int lanes_g = sh.gs / NC;
     const bool runs = p.G > 1 && sh.gs % NC == 0 && (lanes_g & (lanes_g - 1)) == 0;
     for (unsigned todo = __ballot_sync(kFull, (near || near_group) && live && q == 0); todo; todo &= todo - 1) {
@@ -1118,7 +1126,15 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks<NC>) route_backward_
       if (p.z != 0.f && z > 0.f) shared += cz * (m + logf(z));
       const float mean = fp * inv;
 #pragma unroll
-      for (int j = 0; j < NC; ++j) v[j] = v[j] > 0.f ? v[j] * inv * fmaf(cb, f[j] - mean, shared) : 0.f;
+      for (int j = 0; j < NC; ++j) v[j] = v[j] * inv * fmaf(cb, f[j] - mean, shared);
+      if (!(fabsf(shared) < INFINITY)) {  // 0 times that is NaN, and a masked expert's gradient 0
+#pragma unroll 1
+        for (int j = 0; j < NC; ++j) {
+          const bool in = c0 + j < p.E && usable<T>(Elem<T>::to_f(row[c0 + j])) > -INFINITY;
+#pragma unroll
+          for (int i = 0; i < NC; ++i) v[i] = i == j && !in ? 0.f : v[i];
+        }
+      }
     }
     if (p.grad_w) {
       // the picks' parts join the row in shared memory, repeated ids one after the other
@@ -1148,11 +1164,13 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks<NC>) route_backward_
 //   rows    256 fp32,            512 bf16,        128 bf16,      8 fp32,
 //           sigmoid in groups,   sigmoid, bias,   softmax, k 4   softmax, k 2
 //           bias, k 8            k 16
-//   16      4.1 / 8.3            5.4 / 15.1       3.2 / 4.4      2.9 / 3.4
-//   1024    5.8 / 10.2           10.4 / 20.6      3.5 / 4.7      3.2 / 3.6
-//   4096    11.5 / 13.9          19.8 / 25.5      6.3 / 4.9      3.9 / 3.7
-//   8192    18.0 / 17.0          30.0 / 28.0      9.9 / 6.3      6.6 / 3.9
-//   65536   97 / 51              156 / 148        52 / 16.3      41 / 11.2
+//   16      4.3 / 8.7            5.2 / 15.8       3.4 / 3.8      3.0 / 2.8
+//   1024    5.8 / 11.2           10.6 / 21.0      3.5 / 3.9      3.2 / 3.0
+//   4096    11.7 / 13.8          19.3 / 26.1      6.3 / 4.0      3.9 / 3.0
+//   8192    17.5 / 17.3          30.3 / 28.3      10.4 / 5.4     6.6 / 3.1
+//   65536   96 / 53              152 / 150        68 / 13.2      41 / 9.0
+// One bound for all: it is where the widest rows change over; narrow rows
+// without a bias would at 4096 already, for 1 to 2 us.
 constexpr int64_t kTileMinRows = 8192;
 
 // Blocks: a warp per row up to a few resident blocks per SM, then rows in turn
@@ -1190,14 +1208,17 @@ cudaError_t launch_route_topk(const RouteArgs& args, cudaStream_t stream) {
       if constexpr (NC <= 16) {
         if (a.T >= kTileMinRows && tile_shape(a.E, a.G).nb <= 4 * kTileBlocks<NC>) {
           const size_t smem = tile_smem(a.E, a.G);
-          if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(route_tile_kernel<T, NC>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-          }
-          route_tile_kernel<T, NC>
-              <<<(unsigned)((a.T + kTileRows - 1) / kTileRows), kThreads, smem, stream>>>(a);
-          return cudaGetLastError();
+          auto run = [&](auto kernel) {
+            if (smem > 48 * 1024) {
+              const cudaError_t e =
+                  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+              if (e != cudaSuccess) return e;
+            }
+            kernel<<<(unsigned)((a.T + kTileRows - 1) / kTileRows), kThreads, smem, stream>>>(a);
+            return cudaGetLastError();
+          };
+          if (!a.bias && (a.G == 1 || a.group_top == 1)) return run(route_tile_kernel<T, NC, true>);
+          return run(route_tile_kernel<T, NC, false>);
         }
       }
       route_topk_kernel<T, decltype(nc)::value><<<blocks_for(a.T, 12), kThreads, 0, stream>>>(a);
