@@ -357,9 +357,13 @@ moe_status moe_forward_traced(const moe_config* cfg, const void* x, const void* 
    that value (the usual masks) exclude an expert for that token, and so does a
    bias of -inf or NaN.  +inf counts as the largest finite value.  A slot for
    which no expert is left gets id -1 and weight 0, so a row masked throughout
-   (padding) routes nowhere.  Choices are compared as the stored logits define
-   them: without a bias (or with zeros) by their logits, otherwise in binary64
-   wherever fp32 could not tell. */
+   (padding) routes nowhere (moe_permute skips such slots, but reports them as
+   MOE_ERR_BAD_EXPERT_ID; moe_forward_routed does not).  Choices are compared as
+   the stored logits define them: without a bias (or with zeros) by their
+   logits, otherwise, and for sums of two, in binary64 wherever fp32 could not
+   tell.  To switch an expert off for all tokens give it a bias of -inf: a large
+   finite one is right too, but binary64 then decides every row (72 against 16 us
+   for 8192 rows of 256).  Weights and gradients below 2^-126 may come out as 0. */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 
 typedef struct {
